@@ -17,6 +17,19 @@
  * can also run as one kernel that keeps h on chip (moe_expert_ffn_fused,
  * moe_expert_ffn_fp8_fused; same results, no workspace).
  *
+ * Around the experts' matrix products the library also has the layer's row
+ * operators, for serving and for training with a caller's own products:
+ *
+ *   moe_rmsnorm            residual addition + RMS norm, also as e4m3 codes
+ *                          with 1x128 scales (what moe_expert_ffn_fp8 reads)
+ *   moe_dispatch           token rows copied into expert order
+ *   moe_swiglu             SwiGLU, its output also as codes, its input also
+ *                          kept as an 8-bit checkpoint
+ *   moe_rmsnorm_backward, moe_dispatch_backward, moe_swiglu_backward,
+ *   moe_finalize_backward, moe_route_backward
+ *                          their gradients, those of moe_finalize and that of
+ *                          moe_route's weights
+ *
  * Conventions shared by every call:
  *  - Pointers named as device buffers are device pointers (hipMalloc'd or
  *    torch CUDA tensors); scalars are passed by value.  All arrays are dense,
@@ -313,6 +326,189 @@ moe_status moe_expert_ffn_fp8_fused(const uint8_t* xq, const float* x_scale, int
                                     const uint8_t* w2, const float* w13_scale,
                                     const float* w2_scale, int split, void* fc2_out, void* stream);
 
+/*
+ * The row operators below share these rules beyond the ones at the top:
+ *  - dt is MOE_F32 or MOE_BF16; sums, norms and softmax statistics are fp32 or
+ *    wider and every output is rounded once, to its own type.
+ *  - Device pointers of [rows, columns] arrays are 16-byte aligned
+ *    (MOE_ERR_INVALID_ARG otherwise); int32 and fp32 [T, k], [rows, cols/128]
+ *    and [H] arrays of `unpermute`, scales and `dweight` need only their
+ *    element's alignment.
+ *  - An output may not overlap an input or another output except where the
+ *    call says so.
+ *  - Rows are independent: a NaN or infinity in one row changes no other row
+ *    (dweight, which sums over the rows, excepted).
+ */
+
+/* Widest row of moe_rmsnorm and moe_rmsnorm_backward (a row is held in one
+ * workgroup's registers). */
+#define MOE_NORM_MAX_H 16384
+
+/*
+ * moe_rmsnorm -- the norm in front of the layer, with the addition of the
+ * residual stream and, for the fp8 path, the quantise-input step of the
+ * TensorRT-LLM page (section "“自适应顺序”里的一个细节") in the same pass:
+ *     z = x + residual   (rounded to `dt`; z = x without a residual)
+ *     y = z * rsqrt(mean(z^2) + eps) * weight
+ * The norm is taken of the rounded z, the value the residual stream carries
+ * on, so that moe_rmsnorm_backward, which reads it, differentiates the same
+ * function.
+ *
+ *  x         device [T, H] in `dt`.
+ *  residual  device [T, H] in `dt` or NULL.
+ *  weight    device [H] in `dt`, 16-byte aligned.
+ *  H         a multiple of 8 (of 128 with yq), at most MOE_NORM_MAX_H.
+ *  eps       > 0, finite.
+ *  total     device [T, H] in `dt` out: z.  Required with a residual and NULL
+ *            without one; may be x or residual itself (the update in place).
+ *  y         device [T, H] in `dt` out, or NULL; may be x itself where total
+ *            is not.
+ *  yq, y_scale  device uint8 [T, H] and fp32 [T, H/128] out, both or neither:
+ *            the fp32 y (not its `dt` rounding) quantised as moe_quantize_fp8
+ *            does.  At least one of y and yq is given.
+ */
+moe_status moe_rmsnorm(const void* x, const void* residual, const void* weight, int dt, int T, int H,
+                       float eps, void* total, void* y, uint8_t* yq, float* y_scale, void* stream);
+
+/*
+ * moe_rmsnorm_backward -- gradients of moe_rmsnorm (through y):
+ *     c = rsqrt(mean(z^2) + eps),  g = dy * weight
+ *     dz = c g - z c^3 mean(g z) (+ dtotal),   dweight = sum_t dy_t z_t c_t
+ * dz is the gradient of x and of the residual alike.
+ *
+ *  dy       device [T, H] in `dt`: gradient of y.
+ *  z        device [T, H] in `dt`: moe_rmsnorm's total (x without a residual).
+ *  dtotal   device [T, H] in `dt` or NULL: gradient that reaches z through the
+ *           residual stream.
+ *  dz       device [T, H] in `dt` out; may be dy or dtotal itself.
+ *  dweight  device fp32 [H] out.  Summed in an order that depends on the shape
+ *           alone: the same inputs give the same bits.  T == 0 sets it to zero
+ *           (the one launch that T == 0 makes).
+ *  ws       device workspace of moe_rmsnorm_backward_workspace_size(T, H)
+ *           bytes, 16-byte aligned.
+ * H and eps as for moe_rmsnorm.
+ */
+moe_status moe_rmsnorm_backward(const void* dy, const void* z, const void* weight,
+                                const void* dtotal, int dt, int T, int H, float eps, void* dz,
+                                float* dweight, void* ws, size_t ws_bytes, void* stream);
+
+/* Bytes of workspace that moe_rmsnorm_backward needs (0 on invalid arguments
+ * and for T == 0).  Host-only. */
+size_t moe_rmsnorm_backward_workspace_size(int T, int H);
+
+/*
+ * moe_dispatch -- token rows copied into expert order, the rows that FC1 of a
+ * caller's own grouped product (or another device's experts) reads:
+ *     rows[unpermute[t*k + j]] = x[t],   rows[T*k + s*T + t] = x[t]
+ * ("从 Dense GEMM 到 TP MoE 的演进逻辑", section 2.2: permute each expert's
+ * tokens into one block).  moe_expert_ffn itself needs no such copy: it
+ * gathers its rows through permuted_pair.
+ *
+ *  x          device [T, H] in `dt`, which may also be MOE_FP8_E4M3: codes,
+ *             with x_scale [T, H/128], as moe_quantize_fp8 or moe_rmsnorm
+ *             write them.
+ *  H          a multiple of 8 (fp8: of 128).
+ *  unpermute  device int32 [T*k] from moe_permute.  A pair whose entry lies
+ *             outside [0, T*k) is dropped: no row is written for it.
+ *  rows       device [T*k + n_shared*T, H] in `dt` out.  Rows that no pair
+ *             names are left as they were.
+ *  rows_scale device fp32 [T*k + n_shared*T, H/128] out for MOE_FP8_E4M3,
+ *             else NULL (like x_scale).
+ */
+moe_status moe_dispatch(const void* x, const float* x_scale, int dt, int T, int H, int k,
+                        int n_shared, const int32_t* unpermute, void* rows, float* rows_scale,
+                        void* stream);
+
+/*
+ * moe_dispatch_backward -- gradient of moe_dispatch:
+ *     dx[t] = sum_j d_rows[unpermute[t*k + j]] + sum_s d_rows[T*k + s*T + t]
+ * in fp32, j in order, then the shared rows in order (moe_finalize with every
+ * scale 1, except that a dropped pair adds nothing).
+ *
+ *  d_rows  device [T*k + n_shared*T, H] in `dt`.
+ *  dx      device [T, H] in `dxt` (MOE_F32 or MOE_BF16) out.
+ *  H       a multiple of 8.
+ */
+moe_status moe_dispatch_backward(const void* d_rows, int dt, const int32_t* unpermute, int T, int k,
+                                 int H, int n_shared, void* dx, int dxt, void* stream);
+
+/*
+ * moe_finalize_backward -- gradients of moe_finalize:
+ *     d_fc2[unpermute[t*k + j]] = scales[t, j] * dy[t],  d_fc2[T*k + s*T + t] = dy[t]
+ *     d_scales[t, j]            = sum_h dy[t, h] * fc2_out[unpermute[t*k + j], h]
+ *
+ *  dy        device [T, H] in `dyt` (MOE_F32 or MOE_BF16).
+ *  fc2_out   device [T*k + n_shared*T, H] in `dt`, as given to moe_finalize.
+ *  unpermute, scales   as given to moe_finalize.  A dropped pair (entry outside
+ *            [0, T*k)) gets d_scales 0, and no row is written for it.
+ *  d_fc2     device [T*k + n_shared*T, H] in `dt` out; may be fc2_out itself.
+ *  d_scales  device fp32 [T, k] out: what moe_route_backward takes.
+ *  H         a multiple of 8.
+ */
+moe_status moe_finalize_backward(const void* dy, int dyt, const void* fc2_out, int dt,
+                                 const int32_t* unpermute, const float* scales, int T, int k, int H,
+                                 int n_shared, void* d_fc2, float* d_scales, void* stream);
+
+/*
+ * moe_route_backward -- gradient of moe_route's scales with respect to the
+ * logits, the choice of experts held fixed (the correction bias only chooses,
+ * so it has no gradient).  With v_j = scaling * d_scales[t, j] and e_j =
+ * ids[t, j]:
+ *   softmax over all E (DEFAULT without the flag):
+ *       d_e = p_e (v_j if e = e_j else 0) - p_e sum_i v_i p_{e_i}
+ *   softmax over the kept (RENORMALIZE, RENORMALIZE_NAIVE, DEFAULT with the
+ *   flag), q the kept softmax:  d_{e_j} = q_j (v_j - sum_i v_i q_i)
+ *   sigmoids over their sum S (DEEPSEEKV3 with its 1e-20, MINIMAX2,
+ *   SIGMOID_RENORM):  d_{e_j} = sig_j (1 - sig_j) / S (v_j - sum_i v_i sig_i / S)
+ *   LLAMA4:  d_{e_j} = v_j sig_j (1 - sig_j)
+ * and 0 for every other expert.
+ *
+ *  logits, ids   as given to and returned by moe_route.  An id outside [0, E)
+ *            is a dropped pair: it takes no part.  An id that a token lists
+ *            twice gets the sum of both gradients.
+ *  method, k, scaling, flags   as for moe_route.
+ *  d_scales  device fp32 [T, k].
+ *  d_logits  device fp32 [T, E] out, every element written; 16-byte aligned.
+ * Kept logits that are all -infinity give a row of zeros; NaN and +infinity
+ * give unspecified values in their row.
+ */
+moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* d_scales, int T,
+                              int E, int method, int k, float scaling, unsigned flags,
+                              float* d_logits, void* stream);
+
+/*
+ * moe_swiglu -- the experts' activation on the rows of an FC1 product,
+ *     h = silu(gate) * up,   gate = gu[:, 0:I], up = gu[:, I:2I]
+ * (the halves in w13's order), with two 8-bit outputs in moe_quantize_fp8's
+ * format: h for an fp8 FC2, and gu itself as the checkpoint that
+ * moe_swiglu_backward reads instead of gu (1.03 bytes a value).
+ *
+ *  gu        device [rows, 2I] in `dt`.
+ *  I         a multiple of 8, of 128 with any 8-bit output.
+ *  h         device [rows, I] in `dt` out, or NULL.
+ *  hq, h_scale  device uint8 [rows, I], fp32 [rows, I/128] out, both or
+ *            neither: the fp32 h quantised.  At least one of h and hq is given.
+ *  guq, gu_scale  device uint8 [rows, 2I], fp32 [rows, 2I/128] out, both or
+ *            neither: moe_quantize_fp8 of gu, bit for bit.
+ */
+moe_status moe_swiglu(const void* gu, int dt, int rows, int I, void* h, uint8_t* hq, float* h_scale,
+                      uint8_t* guq, float* gu_scale, void* stream);
+
+/*
+ * moe_swiglu_backward -- gradient of the activation at the checkpoint's values
+ * (code * scale), with s = sigmoid(gate):
+ *     d_gate = dh * up * s * (1 + gate * (1 - s)),   d_up = dh * gate * s
+ *
+ *  dh        device [rows, I] in `dt`: gradient of h.
+ *  guq, gu_scale  as written by moe_swiglu or moe_quantize_fp8.
+ *  d_gu      device [rows, 2I] in `dt` out: d_gate, then d_up.
+ *  h         device [rows, I] in `dt` out, or NULL: h of the checkpoint's
+ *            values again, for FC2's weight gradient; may be dh itself.
+ *  I         a multiple of 128.
+ */
+moe_status moe_swiglu_backward(const void* dh, int dt, const uint8_t* guq, const float* gu_scale,
+                               int rows, int I, void* d_gu, void* h, void* stream);
+
 /* Bytes of workspace that moe_permute and moe_expert_ffn need for this shape
  * (0 on invalid arguments).  One buffer of this size serves both calls.
  * act = MOE_FP8_E4M3 sizes it for moe_expert_ffn_fp8.  The size depends only
@@ -351,7 +547,16 @@ enum {
     MOE_KID_QUANT = 7,
     MOE_KID_FFN_FUSED = 8,
     MOE_KID_PERMUTE_ONE = 9,   /* the one-workgroup permute (inputs of up to 8192 pairs) */
-    MOE_NUM_KIDS = 10
+    MOE_KID_RMSNORM = 10,
+    MOE_KID_RMSNORM_BWD = 11,
+    MOE_KID_RMSNORM_DWEIGHT = 12,  /* the sum of moe_rmsnorm_backward's partial dweight rows */
+    MOE_KID_DISPATCH = 13,
+    MOE_KID_DISPATCH_BWD = 14,
+    MOE_KID_FINALIZE_BWD = 15,
+    MOE_KID_ROUTE_BWD = 16,
+    MOE_KID_SWIGLU = 17,
+    MOE_KID_SWIGLU_BWD = 18,
+    MOE_NUM_KIDS = 19
 };
 moe_status moe_timing_enable(int enable);
 moe_status moe_kernel_times(double* ms /*[MOE_NUM_KIDS]*/, int64_t* launches /*[MOE_NUM_KIDS]*/,

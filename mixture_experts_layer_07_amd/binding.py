@@ -21,7 +21,9 @@ F32, BF16, FP8_E4M3 = 0, 1, 2
 ROUTE_DEFAULT, ROUTE_RENORMALIZE, ROUTE_DEEPSEEKV3, ROUTE_RENORMALIZE_NAIVE = 0, 1, 2, 4
 ROUTE_FLAG_RENORMALIZE = 1
 KERNEL_IDS = ["route", "permute_count", "permute_scan", "permute_scatter", "fc1", "fc2",
-              "finalize", "quantize", "ffn_fused", "permute_one"]
+              "finalize", "quantize", "ffn_fused", "permute_one", "rmsnorm", "rmsnorm_backward",
+              "rmsnorm_dweight", "dispatch", "dispatch_backward", "finalize_backward",
+              "route_backward", "swiglu", "swiglu_backward"]
 FUSED_MAX_I = 2048
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
@@ -53,6 +55,16 @@ def lib():
         L.moe_expert_ffn_noalloc.argtypes = [P, i, i, i, i, i, i, i, P, P, P, P, i, P, P, P, P]
         L.moe_expert_ffn_fused.argtypes = [P, i, i, i, i, i, i, i, P, P, P, P, i, P, P, i, P, P]
         L.moe_expert_ffn_fp8_fused.argtypes = [P, P, i, i, i, i, i, i, P, P, P, P, P, P, i, P, P]
+        L.moe_rmsnorm.argtypes = [P, P, P, i, i, i, f, P, P, P, P, P]
+        L.moe_rmsnorm_backward.argtypes = [P, P, P, P, i, i, i, f, P, P, P, z, P]
+        L.moe_rmsnorm_backward_workspace_size.argtypes = [i, i]
+        L.moe_rmsnorm_backward_workspace_size.restype = z
+        L.moe_dispatch.argtypes = [P, P, i, i, i, i, i, P, P, P, P]
+        L.moe_dispatch_backward.argtypes = [P, i, P, i, i, i, i, P, i, P]
+        L.moe_finalize_backward.argtypes = [P, i, P, i, P, P, i, i, i, i, P, P, P]
+        L.moe_route_backward.argtypes = [P, P, P, i, i, i, i, f, u, P, P]
+        L.moe_swiglu.argtypes = [P, i, i, i, P, P, P, P, P, P]
+        L.moe_swiglu_backward.argtypes = [P, i, P, P, i, i, P, P, P]
         L.moe_workspace_size.argtypes = [i, i, i, i, i, i, i]
         L.moe_workspace_size.restype = z
         L.moe_status_string.argtypes = [i]
@@ -63,8 +75,10 @@ def lib():
         L.moe_kernel_times.argtypes = [P, P, i]
         for fn in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_expert_ffn_noalloc", "moe_finalize",
                    "moe_quantize_fp8", "moe_expert_ffn_fp8", "moe_expert_ffn_fused",
-                   "moe_expert_ffn_fp8_fused", "moe_timing_enable",
-                   "moe_kernel_times"):
+                   "moe_expert_ffn_fp8_fused", "moe_rmsnorm", "moe_rmsnorm_backward",
+                   "moe_dispatch", "moe_dispatch_backward", "moe_finalize_backward",
+                   "moe_route_backward", "moe_swiglu", "moe_swiglu_backward",
+                   "moe_timing_enable", "moe_kernel_times"):
             getattr(L, fn).restype = C.c_int
         _lib = L
     return _lib
@@ -342,6 +356,202 @@ def finalize(fc2_out, unpermute, scales, n_shared=0, out_dtype=None, out=None):
     _call("moe_finalize", fc2_out.device, fc2_out, _DT[fc2_out.dtype], unpermute, scales, T, k, H,
           n_shared, out, _DT[ydt])
     return out
+
+
+# ----------------------------------------------------------- row operators
+def _out(t, name, shape, dtype, device):
+    """The caller's output buffer `t`, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _dev(t, name, dtype, shape)
+
+
+def _rows_of(x, name, dtype):
+    _dev(x, name, dtype)
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [rows, columns] (got {tuple(x.shape)})")
+    return x.shape
+
+
+def _places(unpermute, k):
+    """T of a moe_permute result."""
+    _dev(unpermute, "unpermute", torch.int32)
+    if k < 1 or unpermute.dim() != 1 or unpermute.numel() % k:
+        raise ValueError(f"unpermute must be [T * k] (got {tuple(unpermute.shape)}, k = {k})")
+    return unpermute.numel() // k
+
+
+def _unused(names, given):
+    for name, t in zip(names, given):
+        if t is not None:
+            raise ValueError(f"out: {name} is not an output of this call")
+
+
+_ACT = (torch.float32, torch.bfloat16)
+
+
+def rmsnorm(x, weight, eps=1e-6, residual=None, quantize=False, want_y=True, out=None):
+    """moe_rmsnorm -> (y, total, yq, y_scale): y = rmsnorm(total) * weight with total = x + residual
+    (None without a residual), and with quantize the e4m3 codes and 1x128 scales of y that
+    expert_ffn_fp8 takes (else None, None).  want_y=False writes the codes alone (y None).
+    `out` is the same tuple of buffers; out's total may be x or residual."""
+    T, H = _rows_of(x, "x", _ACT)
+    dt, d = x.dtype, x.device
+    _dev(weight, "weight", dt, (H,))
+    if residual is not None:
+        _dev(residual, "residual", dt, (T, H))
+    y, total, yq, ys = (None,) * 4 if out is None else out
+    if want_y:
+        y = _out(y, "y", (T, H), dt, d)
+    else:
+        _unused(("y",), (y,))
+    if residual is not None:
+        total = _out(total, "total", (T, H), dt, d)
+    else:
+        _unused(("total",), (total,))
+    if quantize:
+        yq = _out(yq, "yq", (T, H), torch.float8_e4m3fn, d)
+        ys = _out(ys, "y_scale", (T, H // 128), torch.float32, d)
+    else:
+        _unused(("yq", "y_scale"), (yq, ys))
+    _call("moe_rmsnorm", d, x, residual, weight, _DT[dt], T, H, float(eps), total, y, yq, ys)
+    return y, total, yq, ys
+
+
+def rmsnorm_backward_workspace(T, H, device="cuda") -> torch.Tensor:
+    n = int(lib().moe_rmsnorm_backward_workspace_size(T, H))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def rmsnorm_backward(dy, z, weight, eps=1e-6, dsum=None, ws=None, out=None):
+    """moe_rmsnorm_backward -> (dz [T, H], dweight fp32 [H]): z is rmsnorm's total (x without a
+    residual), dz the gradient of x and of the residual alike, dsum the gradient that reaches z
+    through the residual stream.  out's dz may be dy or dsum."""
+    T, H = _rows_of(z, "z", _ACT)
+    dt, d = z.dtype, z.device
+    _dev(dy, "dy", dt, (T, H))
+    _dev(weight, "weight", dt, (H,))
+    if dsum is not None:
+        _dev(dsum, "dsum", dt, (T, H))
+    dz, dw = (None, None) if out is None else out
+    dz = _out(dz, "dz", (T, H), dt, d)
+    dw = _out(dw, "dweight", (H,), torch.float32, d)
+    if ws is None:
+        ws = rmsnorm_backward_workspace(T, H, d)
+    _dev(ws, "ws", torch.uint8)
+    _call("moe_rmsnorm_backward", d, dy, z, weight, dsum, _DT[dt], T, H, float(eps), dz, dw, ws, ws.numel())
+    return dz, dw
+
+
+def dispatch(x, unpermute, k, n_shared=0, x_scale=None, out=None):
+    """moe_dispatch -> rows [T*k + n_shared*T, H] in expert order; for e4m3 codes x with their
+    x_scale -> (rows, rows_scale), and `out` is such a pair."""
+    T, H = _rows_of(x, "x", (torch.float32, torch.bfloat16, torch.float8_e4m3fn))
+    d, fp8 = x.device, x.dtype == torch.float8_e4m3fn
+    if _places(unpermute, k) != T:
+        raise ValueError(f"unpermute has {unpermute.numel()} pairs, expected {T * k}")
+    R = T * k + n_shared * T
+    if fp8 != (x_scale is not None):
+        raise ValueError("x_scale goes with float8_e4m3fn x, and only with it")
+    scale = None
+    if fp8:
+        _dev(x_scale, "x_scale", torch.float32, (T, H // 128))
+        out, scale = (None, None) if out is None else out
+        scale = _out(scale, "rows_scale", (R, H // 128), torch.float32, d)
+    out = _out(out, "rows", (R, H), x.dtype, d)
+    _call("moe_dispatch", d, x, x_scale, _DT[x.dtype], T, H, k, n_shared, unpermute, out, scale)
+    return (out, scale) if fp8 else out
+
+
+def dispatch_backward(d_rows, unpermute, k, n_shared=0, out_dtype=None, out=None):
+    """moe_dispatch_backward -> dx [T, H]: each token's rows summed."""
+    R, H = _rows_of(d_rows, "d_rows", _ACT)
+    T = _places(unpermute, k)
+    if R != T * k + n_shared * T:
+        raise ValueError(f"d_rows has {R} rows, expected {T * k + n_shared * T}")
+    dt = out_dtype or d_rows.dtype
+    out = _out(out, "dx", (T, H), dt, d_rows.device)
+    _call("moe_dispatch_backward", d_rows.device, d_rows, _DT[d_rows.dtype], unpermute, T, k, H,
+          n_shared, out, _DT[dt])
+    return out
+
+
+def finalize_backward(dy, fc2_out, unpermute, scales, n_shared=0, out=None):
+    """moe_finalize_backward -> (d_fc2 [T*k + n_shared*T, H] in fc2_out's dtype, d_scales fp32 [T, k]).
+    out's d_fc2 may be fc2_out."""
+    _dev(scales, "scales", torch.float32)
+    T, k = scales.shape
+    R, H = _rows_of(fc2_out, "fc2_out", _ACT)
+    _dev(dy, "dy", _ACT, (T, H))
+    _dev(unpermute, "unpermute", torch.int32, (T * k,))
+    if R != T * k + n_shared * T:
+        raise ValueError(f"fc2_out has {R} rows, expected {T * k + n_shared * T}")
+    d = fc2_out.device
+    d_fc2, d_scales = (None, None) if out is None else out
+    d_fc2 = _out(d_fc2, "d_fc2", (R, H), fc2_out.dtype, d)
+    d_scales = _out(d_scales, "d_scales", (T, k), torch.float32, d)
+    _call("moe_finalize_backward", d, dy, _DT[dy.dtype], fc2_out, _DT[fc2_out.dtype], unpermute, scales,
+          T, k, H, n_shared, d_fc2, d_scales)
+    return d_fc2, d_scales
+
+
+def route_backward(logits, ids, d_scales, method, scaling=1.0, renormalize=False, out=None):
+    """moe_route_backward -> d_logits fp32 [T, E] from the gradient of route's scales."""
+    T, E = _rows_of(logits, "logits", torch.float32)
+    _dev(ids, "ids", torch.int32)
+    k = ids.shape[1] if ids.dim() == 2 else 0
+    _dev(ids, "ids", shape=(T, k))
+    _dev(d_scales, "d_scales", torch.float32, (T, k))
+    out = _out(out, "d_logits", (T, E), torch.float32, logits.device)
+    _call("moe_route_backward", logits.device, logits, ids, d_scales, T, E, method, k, float(scaling),
+          ROUTE_FLAG_RENORMALIZE if renormalize else 0, out)
+    return out
+
+
+def swiglu(gu, quantize=False, checkpoint=False, want_h=None, out=None):
+    """moe_swiglu -> (h, hq, h_scale, guq, gu_scale) of FC1 rows gu [rows, 2I] (gate, then up):
+    h in gu's dtype, with quantize its e4m3 codes and 1x128 scales instead (want_h=True: both),
+    with checkpoint the codes and scales of gu for swiglu_backward; the others None.  `out` is the
+    same tuple of buffers."""
+    rows, I2 = _rows_of(gu, "gu", _ACT)
+    if I2 % 2:
+        raise ValueError(f"gu must be [rows, 2I] (got {tuple(gu.shape)})")
+    I, dt, d = I2 // 2, gu.dtype, gu.device
+    want_h = not quantize if want_h is None else want_h
+    h, hq, hs, q, qs = (None,) * 5 if out is None else out
+    if want_h:
+        h = _out(h, "h", (rows, I), dt, d)
+    else:
+        _unused(("h",), (h,))
+    if quantize:
+        hq = _out(hq, "hq", (rows, I), torch.float8_e4m3fn, d)
+        hs = _out(hs, "h_scale", (rows, I // 128), torch.float32, d)
+    else:
+        _unused(("hq", "h_scale"), (hq, hs))
+    if checkpoint:
+        q = _out(q, "guq", (rows, I2), torch.float8_e4m3fn, d)
+        qs = _out(qs, "gu_scale", (rows, I2 // 128), torch.float32, d)
+    else:
+        _unused(("guq", "gu_scale"), (q, qs))
+    _call("moe_swiglu", d, gu, _DT[dt], rows, I, h, hq, hs, q, qs)
+    return h, hq, hs, q, qs
+
+
+def swiglu_backward(dh, guq, gu_scale, want_h=False, out=None):
+    """moe_swiglu_backward -> (d_gu [rows, 2I], h [rows, I] or None) from swiglu's checkpoint;
+    with want_h the checkpoint's h again, for FC2's weight gradient (out's h may be dh)."""
+    rows, I = _rows_of(dh, "dh", _ACT)
+    dt, d = dh.dtype, dh.device
+    _dev(guq, "guq", torch.float8_e4m3fn, (rows, 2 * I))
+    _dev(gu_scale, "gu_scale", torch.float32, (rows, 2 * I // 128))
+    d_gu, h = (None, None) if out is None else out
+    d_gu = _out(d_gu, "d_gu", (rows, 2 * I), dt, d)
+    if want_h:
+        h = _out(h, "h", (rows, I), dt, d)
+    else:
+        _unused(("h",), (h,))
+    _call("moe_swiglu_backward", d, dh, _DT[dt], guq, gu_scale, rows, I, d_gu, h)
+    return d_gu, h
 
 
 def timing_enable(on: bool = True):

@@ -12,7 +12,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.hip", "route.hip", "permute.hip", "ffn.hip", "fused.hip", "finalize.hip",
-           "quant.hip", "noalloc.hip"]
+           "quant.hip", "noalloc.hip", "norm.hip", "dispatch.hip", "swiglu.hip", "route_backward.hip"]
 CALIB_SOURCE = "calib.hip"
 CALIB_LIB = os.path.join(HERE, "libmoe_calib.so")
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")

@@ -6,6 +6,7 @@
 #include <stdio.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 #include <vector>
 
@@ -404,6 +405,207 @@ moe_status moe_finalize(const void* fc2_out, int dt, const int32_t* unpermute,
         return set_error(MOE_ERR_INVALID_ARG, "fc2_out, unpermute, scales and y must be non-null");
     return launch_finalize(fc2_out, dt, unpermute, scales, T, k, H, n_shared, y, ydt,
                            static_cast<hipStream_t>(stream));
+}
+
+// ------------------------------------------------------------ row operators
+// Every pointer that is read or written in 16-byte words; a null one passes.
+static bool aligned16(std::initializer_list<const void*> ps)
+{
+    uintptr_t bits = 0;
+    for (const void* p : ps) bits |= reinterpret_cast<uintptr_t>(p);
+    return (bits & 15) == 0;
+}
+
+static moe_status misaligned()
+{
+    return set_error(MOE_ERR_INVALID_ARG, "[rows, columns] buffers must be 16-byte aligned");
+}
+
+static moe_status check_rows(const char* name, int rows)
+{
+    if (rows < 0) return set_error(MOE_ERR_INVALID_ARG, "%s must be >= 0 (got %d)", name, rows);
+    if (rows > (1 << 30)) return set_error(MOE_ERR_UNSUPPORTED, "%s = %d exceeds 2^30 rows", name, rows);
+    return MOE_OK;
+}
+
+static moe_status check_norm(int dt, int T, int H, float eps)
+{
+    moe_status st = check_rows("T", T);
+    if (st != MOE_OK) return st;
+    if (!valid_act(dt)) return set_error(MOE_ERR_INVALID_ARG, "dtype %d must be MOE_F32 or MOE_BF16", dt);
+    if (H < 1) return set_error(MOE_ERR_INVALID_ARG, "H must be positive (got %d)", H);
+    if (H % 8) return set_error(MOE_ERR_UNSUPPORTED, "H must be a multiple of 8 (got %d)", H);
+    if (H > MOE_NORM_MAX_H)
+        return set_error(MOE_ERR_UNSUPPORTED, "H = %d exceeds the norm's limit %d (a row is held in registers)", H,
+                         MOE_NORM_MAX_H);
+    if (!(eps > 0.0f) || !isfinite(eps)) return set_error(MOE_ERR_INVALID_ARG, "eps must be positive and finite");
+    return MOE_OK;
+}
+
+moe_status moe_rmsnorm(const void* x, const void* residual, const void* weight, int dt, int T, int H,
+                       float eps, void* total, void* y, uint8_t* yq, float* y_scale, void* stream)
+{
+    moe_status st = check_norm(dt, T, H, eps);
+    if (st != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    if (!x || !weight) return set_error(MOE_ERR_INVALID_ARG, "x and weight must be non-null");
+    if (!residual != !total)
+        return set_error(MOE_ERR_INVALID_ARG, "residual and total must be given together or not at all");
+    if (!yq != !y_scale) return set_error(MOE_ERR_INVALID_ARG, "yq and y_scale must be given together or not at all");
+    if (!y && !yq) return set_error(MOE_ERR_INVALID_ARG, "y or yq must be given");
+    if (y && y == total) return set_error(MOE_ERR_INVALID_ARG, "y and total must be different buffers");
+    if (yq && H % 128) return set_error(MOE_ERR_UNSUPPORTED, "H must be a multiple of 128 with yq (got %d)", H);
+    if (!aligned16({x, residual, weight, total, y, yq})) return misaligned();
+    return launch_rmsnorm(x, residual, weight, dt, T, H, eps, total, y, yq, y_scale,
+                          static_cast<hipStream_t>(stream));
+}
+
+size_t moe_rmsnorm_backward_workspace_size(int T, int H)
+{
+    if (check_norm(MOE_BF16, T, H, 1.0f) != MOE_OK || T == 0) return 0;
+    return rmsnorm_backward_scratch_bytes(T, H);
+}
+
+moe_status moe_rmsnorm_backward(const void* dy, const void* z, const void* weight,
+                                const void* dtotal, int dt, int T, int H, float eps, void* dz,
+                                float* dweight, void* ws, size_t ws_bytes, void* stream)
+{
+    moe_status st = check_norm(dt, T, H, eps);
+    if (st != MOE_OK) return st;
+    if (!dweight) return set_error(MOE_ERR_INVALID_ARG, "dweight must be non-null");
+    if (T > 0) {
+        if (!dy || !z || !weight || !dz)
+            return set_error(MOE_ERR_INVALID_ARG, "dy, z, weight and dz must be non-null");
+        if (!aligned16({dy, z, weight, dtotal, dz, ws})) return misaligned();
+        const size_t need = rmsnorm_backward_scratch_bytes(T, H);
+        if (!ws || ws_bytes < need)
+            return set_error(MOE_ERR_WORKSPACE, "rmsnorm_backward needs %zu workspace bytes (got %zu)", need,
+                             ws_bytes);
+    }
+    return launch_rmsnorm_backward(dy, z, weight, dtotal, dt, T, H, eps, dz, dweight, ws,
+                                   static_cast<hipStream_t>(stream));
+}
+
+static moe_status check_places(int T, int k, int H, int n_shared)
+{
+    if (T < 0) return set_error(MOE_ERR_INVALID_ARG, "T must be >= 0 (got %d)", T);
+    if (k < 1) return set_error(MOE_ERR_INVALID_ARG, "k must be >= 1 (got %d)", k);
+    if (k > MOE_MAX_TOPK) return set_error(MOE_ERR_UNSUPPORTED, "k = %d exceeds the kernel limit %d", k, MOE_MAX_TOPK);
+    if (n_shared < 0 || n_shared > 64) return set_error(MOE_ERR_INVALID_ARG, "n_shared must be in [0, 64]");
+    if (H < 1) return set_error(MOE_ERR_INVALID_ARG, "H must be positive");
+    if (H % 8) return set_error(MOE_ERR_UNSUPPORTED, "H must be a multiple of 8 (got %d)", H);
+    if ((long long)T * k + (long long)n_shared * T > (1ll << 30))
+        return set_error(MOE_ERR_UNSUPPORTED, "too many rows");
+    return MOE_OK;
+}
+
+moe_status moe_dispatch(const void* x, const float* x_scale, int dt, int T, int H, int k,
+                        int n_shared, const int32_t* unpermute, void* rows, float* rows_scale,
+                        void* stream)
+{
+    moe_status st = check_places(T, k, H, n_shared);
+    if (st != MOE_OK) return st;
+    if (!valid_act(dt) && dt != MOE_FP8_E4M3)
+        return set_error(MOE_ERR_INVALID_ARG, "unknown dtype %d", dt);
+    if (dt == MOE_FP8_E4M3 && H % 128)
+        return set_error(MOE_ERR_UNSUPPORTED, "H must be a multiple of 128 for fp8 rows (got %d)", H);
+    if (T == 0) return MOE_OK;
+    if (!x || !unpermute || !rows) return set_error(MOE_ERR_INVALID_ARG, "x, unpermute and rows must be non-null");
+    if (dt == MOE_FP8_E4M3 ? !x_scale || !rows_scale : x_scale || rows_scale)
+        return set_error(MOE_ERR_INVALID_ARG, "x_scale and rows_scale go with fp8 rows, and only with them");
+    if (!aligned16({x, rows})) return misaligned();
+    return launch_dispatch(x, x_scale, dt, T, H, k, n_shared, unpermute, rows, rows_scale,
+                           static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_dispatch_backward(const void* d_rows, int dt, const int32_t* unpermute, int T, int k,
+                                 int H, int n_shared, void* dx, int dxt, void* stream)
+{
+    moe_status st = check_places(T, k, H, n_shared);
+    if (st != MOE_OK) return st;
+    if (!valid_act(dt) || !valid_act(dxt))
+        return set_error(MOE_ERR_INVALID_ARG, "d_rows and dx dtypes must be MOE_F32 or MOE_BF16");
+    if (T == 0) return MOE_OK;
+    if (!d_rows || !unpermute || !dx)
+        return set_error(MOE_ERR_INVALID_ARG, "d_rows, unpermute and dx must be non-null");
+    if (!aligned16({d_rows, dx})) return misaligned();
+    return launch_dispatch_backward(d_rows, dt, unpermute, T, k, H, n_shared, dx, dxt,
+                                    static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_finalize_backward(const void* dy, int dyt, const void* fc2_out, int dt,
+                                 const int32_t* unpermute, const float* scales, int T, int k, int H,
+                                 int n_shared, void* d_fc2, float* d_scales, void* stream)
+{
+    moe_status st = check_places(T, k, H, n_shared);
+    if (st != MOE_OK) return st;
+    if (!valid_act(dt) || !valid_act(dyt))
+        return set_error(MOE_ERR_INVALID_ARG, "dy and fc2_out dtypes must be MOE_F32 or MOE_BF16");
+    if (T == 0) return MOE_OK;
+    if (!dy || !fc2_out || !unpermute || !scales || !d_fc2 || !d_scales)
+        return set_error(MOE_ERR_INVALID_ARG, "dy, fc2_out, unpermute, scales, d_fc2 and d_scales must be non-null");
+    if (!aligned16({dy, fc2_out, d_fc2})) return misaligned();
+    return launch_finalize_backward(dy, dyt, fc2_out, dt, unpermute, scales, T, k, H, n_shared, d_fc2, d_scales,
+                                    static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_route_backward(const float* logits, const int32_t* ids, const float* d_scales, int T,
+                              int E, int method, int k, float scaling, unsigned flags,
+                              float* d_logits, void* stream)
+{
+    moe_status st = check_common(T, k, E, 0);
+    if (st != MOE_OK) return st;
+    if (method == 7 || method == 8)
+        return set_error(MOE_ERR_UNSUPPORTED, "routing method %d is not implemented (supported: 0-6)", method);
+    if (method < MOE_ROUTE_DEFAULT || method > MOE_ROUTE_SIGMOID_RENORM)
+        return set_error(MOE_ERR_INVALID_ARG, "unknown routing method %d", method);
+    if (flags & ~MOE_ROUTE_FLAG_RENORMALIZE)
+        return set_error(MOE_ERR_INVALID_ARG, "unknown routing flags 0x%x", flags);
+    if (!isfinite(scaling)) return set_error(MOE_ERR_INVALID_ARG, "scaling must be finite");
+    if (T == 0) return MOE_OK;
+    if (!logits || !ids || !d_scales || !d_logits)
+        return set_error(MOE_ERR_INVALID_ARG, "logits, ids, d_scales and d_logits must be non-null");
+    if (!aligned16({d_logits})) return set_error(MOE_ERR_INVALID_ARG, "d_logits must be 16-byte aligned");
+    return launch_route_backward(logits, ids, d_scales, T, E, method, k, scaling, flags, d_logits,
+                                 static_cast<hipStream_t>(stream));
+}
+
+static moe_status check_swiglu(int dt, int rows, int I, bool blocks)
+{
+    moe_status st = check_rows("rows", rows);
+    if (st != MOE_OK) return st;
+    if (!valid_act(dt)) return set_error(MOE_ERR_INVALID_ARG, "dtype %d must be MOE_F32 or MOE_BF16", dt);
+    if (I < 1) return set_error(MOE_ERR_INVALID_ARG, "I must be positive (got %d)", I);
+    if (I > (1 << 29)) return set_error(MOE_ERR_UNSUPPORTED, "I = %d exceeds 2^29", I);
+    if (I % (blocks ? 128 : 8))
+        return set_error(MOE_ERR_UNSUPPORTED, "I must be a multiple of %d (got %d)", blocks ? 128 : 8, I);
+    return MOE_OK;
+}
+
+moe_status moe_swiglu(const void* gu, int dt, int rows, int I, void* h, uint8_t* hq, float* h_scale,
+                      uint8_t* guq, float* gu_scale, void* stream)
+{
+    moe_status st = check_swiglu(dt, rows, I, hq || guq);
+    if (st != MOE_OK) return st;
+    if (rows == 0) return MOE_OK;
+    if (!gu) return set_error(MOE_ERR_INVALID_ARG, "gu must be non-null");
+    if (!h && !hq) return set_error(MOE_ERR_INVALID_ARG, "h or hq must be given");
+    if (!hq != !h_scale || !guq != !gu_scale)
+        return set_error(MOE_ERR_INVALID_ARG, "codes and their scales must be given together or not at all");
+    if (!aligned16({gu, h, hq, guq})) return misaligned();
+    return launch_swiglu(gu, dt, rows, I, h, hq, h_scale, guq, gu_scale, static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_swiglu_backward(const void* dh, int dt, const uint8_t* guq, const float* gu_scale,
+                               int rows, int I, void* d_gu, void* h, void* stream)
+{
+    moe_status st = check_swiglu(dt, rows, I, true);
+    if (st != MOE_OK) return st;
+    if (rows == 0) return MOE_OK;
+    if (!dh || !guq || !gu_scale || !d_gu)
+        return set_error(MOE_ERR_INVALID_ARG, "dh, guq, gu_scale and d_gu must be non-null");
+    if (!aligned16({dh, guq, d_gu, h})) return misaligned();
+    return launch_swiglu_backward(dh, dt, guq, gu_scale, rows, I, d_gu, h, static_cast<hipStream_t>(stream));
 }
 
 moe_status moe_timing_enable(int enable)

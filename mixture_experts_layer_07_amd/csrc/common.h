@@ -142,5 +142,25 @@ moe_status launch_quantize_fp8(const void* x, int dt, int rows, int cols, uint8_
 moe_status launch_finalize(const void* fc2_out, int dt, const int32_t* unpermute,
                            const float* scales, int T, int k, int H, int n_shared, void* y,
                            int ydt, hipStream_t s);
+moe_status launch_rmsnorm(const void* x, const void* residual, const void* weight, int dt, int T, int H,
+                          float eps, void* total, void* y, uint8_t* yq, float* y_scale, hipStream_t s);
+size_t rmsnorm_backward_scratch_bytes(int T, int H);
+moe_status launch_rmsnorm_backward(const void* dy, const void* z, const void* weight, const void* dtotal,
+                                   int dt, int T, int H, float eps, void* dz, float* dweight, void* ws,
+                                   hipStream_t s);
+moe_status launch_dispatch(const void* x, const float* x_scale, int dt, int T, int H, int k, int n_shared,
+                           const int32_t* unpermute, void* rows, float* rows_scale, hipStream_t s);
+moe_status launch_dispatch_backward(const void* d_rows, int dt, const int32_t* unpermute, int T, int k, int H,
+                                    int n_shared, void* dx, int dxt, hipStream_t s);
+moe_status launch_finalize_backward(const void* dy, int dyt, const void* fc2, int dt, const int32_t* unpermute,
+                                    const float* scales, int T, int k, int H, int n_shared, void* d_fc2,
+                                    float* d_scales, hipStream_t s);
+moe_status launch_route_backward(const float* logits, const int32_t* ids, const float* d_scales, int T, int E,
+                                 int method, int k, float scaling, unsigned flags, float* d_logits,
+                                 hipStream_t s);
+moe_status launch_swiglu(const void* gu, int dt, int rows, int I, void* h, uint8_t* hq, float* h_scale,
+                         uint8_t* guq, float* gu_scale, hipStream_t s);
+moe_status launch_swiglu_backward(const void* dh, int dt, const uint8_t* guq, const float* gu_scale, int rows,
+                                  int I, void* d_gu, void* h, hipStream_t s);
 
 }  // namespace moe

@@ -1,0 +1,174 @@
+// moe_swiglu and its gradient from the 8-bit checkpoint.
+//
+//     h = g s u,  s = 1 / (1 + e^-g)
+//     d_g = dh u s (1 + g (1 - s)),  d_u = dh g s
+//
+// Element by element, HBM-bound.  A thread takes 8 gates and the 8 ups of the
+// same columns; 16 consecutive lanes hold one 128-value block of each, so the
+// block maxima stay inside the vector unit.  A thread's chunk (row, col) moves
+// by a fixed stride a step; the stride's whole rows and rest come from the
+// host, so no division is made in the loop.
+#include <algorithm>
+
+#include "rowops.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+// e^-g: bf16 outputs keep 9 bits, so the product form of exp (relative error
+// below 2^-22 |g|) serves; fp32 outputs take the library's function.
+template <class T>
+__device__ __forceinline__ float exp_neg(float g)
+{
+    if constexpr (sizeof(T) == 2) return __expf(-g);
+    else return expf(-g);
+}
+
+template <class T>
+__device__ __forceinline__ float sigmoid(float g)
+{
+    if constexpr (sizeof(T) == 2) return __builtin_amdgcn_rcpf(1.0f + exp_neg<T>(g));
+    else return 1.0f / (1.0f + exp_neg<T>(g));
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void swiglu_kernel(const T* __restrict__ gu, int rows, int nch, int drow,
+                                                          int dcol, T* __restrict__ h, uint8_t* __restrict__ hq,
+                                                          float* __restrict__ h_scale, uint8_t* __restrict__ guq,
+                                                          float* __restrict__ gu_scale)
+{
+    const unsigned first = blockIdx.x * kThreads + threadIdx.x;
+    int row = (int)(first / (unsigned)nch), col = (int)(first % (unsigned)nch);
+    const size_t I = (size_t)nch * 8;
+    while (row < rows) {
+        const size_t g0 = (size_t)row * 2 * I + 8 * col, h0 = (size_t)row * I + 8 * col;
+        Raw8<T> rg, ru;
+        rg.load(gu + g0);
+        ru.load(gu + g0 + I);
+        float g[8], u[8], o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            g[e] = rg[e];
+            u[e] = ru[e];
+            o[e] = g[e] * sigmoid<T>(g[e]) * u[e];
+        }
+        if (h) {
+            Raw8<T> w;
+            w.set(o);
+            w.store(h + h0);
+        }
+        // 8-bit outputs: I is a multiple of 128, so 16 lanes share a row and a block
+        if (hq) {
+            const float s = max16(absmax8(o)) / 448.0f;
+            *reinterpret_cast<uint2*>(hq + h0) = fp8x8_code(o, s);
+            if ((col & 15) == 0) h_scale[h0 >> 7] = s;
+        }
+        if (guq) {
+            const float sg = max16(absmax8(g)) / 448.0f, su = max16(absmax8(u)) / 448.0f;
+            *reinterpret_cast<uint2*>(guq + g0) = fp8x8_code(g, sg);
+            *reinterpret_cast<uint2*>(guq + g0 + I) = fp8x8_code(u, su);
+            if ((col & 15) == 0) {
+                gu_scale[g0 >> 7] = sg;
+                gu_scale[(g0 + I) >> 7] = su;
+            }
+        }
+        row += drow;
+        col += dcol;
+        if (col >= nch) {
+            col -= nch;
+            ++row;
+        }
+    }
+}
+
+// No __restrict__ on dh and h: they may be the same rows.
+template <class T>
+__global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(const T* dh, const uint8_t* __restrict__ guq,
+                                                                   const float* __restrict__ gu_scale, int rows,
+                                                                   int nch, int drow, int dcol,
+                                                                   T* __restrict__ d_gu, T* h)
+{
+    const unsigned first = blockIdx.x * kThreads + threadIdx.x;
+    int row = (int)(first / (unsigned)nch), col = (int)(first % (unsigned)nch);
+    const size_t I = (size_t)nch * 8;
+    while (row < rows) {
+        const size_t g0 = (size_t)row * 2 * I + 8 * col, h0 = (size_t)row * I + 8 * col;
+        Raw8<T> rd;
+        rd.load(dh + h0);
+        const uint2 qg = *reinterpret_cast<const uint2*>(guq + g0);
+        const uint2 qu = *reinterpret_cast<const uint2*>(guq + g0 + I);
+        float g[8], u[8], dg[8], du[8], o[8];
+        fp8x8_value(qg, gu_scale[g0 >> 7], g);
+        fp8x8_value(qu, gu_scale[(g0 + I) >> 7], u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float s = sigmoid<T>(g[e]), gs = g[e] * s, d = rd[e];
+            dg[e] = d * u[e] * (s + gs * (1.0f - s));
+            du[e] = d * gs;
+            o[e] = gs * u[e];
+        }
+        Raw8<T> w;
+        w.set(dg);
+        w.store(d_gu + g0);
+        w.set(du);
+        w.store(d_gu + g0 + I);
+        if (h) {
+            w.set(o);
+            w.store(h + h0);
+        }
+        row += drow;
+        col += dcol;
+        if (col >= nch) {
+            col -= nch;
+            ++row;
+        }
+    }
+}
+
+int grid_of(int rows, int nch)
+{
+    const long chunks = (long)rows * nch;
+    return (int)std::min((chunks + kThreads - 1) / kThreads, 1l << 20);
+}
+
+}  // namespace
+
+moe_status launch_swiglu(const void* gu, int dt, int rows, int I, void* h, uint8_t* hq, float* h_scale,
+                         uint8_t* guq, float* gu_scale, hipStream_t s)
+{
+    const int nch = I / 8, grid = grid_of(rows, nch), stride = grid * kThreads;
+    {
+        TimedLaunch tl(MOE_KID_SWIGLU, s);
+        if (dt == MOE_BF16)
+            hipLaunchKernelGGL(swiglu_kernel<bf16_t>, dim3(grid), dim3(kThreads), 0, s,
+                               static_cast<const bf16_t*>(gu), rows, nch, stride / nch, stride % nch,
+                               static_cast<bf16_t*>(h), hq, h_scale, guq, gu_scale);
+        else
+            hipLaunchKernelGGL(swiglu_kernel<float>, dim3(grid), dim3(kThreads), 0, s,
+                               static_cast<const float*>(gu), rows, nch, stride / nch, stride % nch,
+                               static_cast<float*>(h), hq, h_scale, guq, gu_scale);
+    }
+    return launch_status("swiglu_kernel");
+}
+
+moe_status launch_swiglu_backward(const void* dh, int dt, const uint8_t* guq, const float* gu_scale, int rows,
+                                  int I, void* d_gu, void* h, hipStream_t s)
+{
+    const int nch = I / 8, grid = grid_of(rows, nch), stride = grid * kThreads;
+    {
+        TimedLaunch tl(MOE_KID_SWIGLU_BWD, s);
+        if (dt == MOE_BF16)
+            hipLaunchKernelGGL(swiglu_backward_kernel<bf16_t>, dim3(grid), dim3(kThreads), 0, s,
+                               static_cast<const bf16_t*>(dh), guq, gu_scale, rows, nch, stride / nch,
+                               stride % nch, static_cast<bf16_t*>(d_gu), static_cast<bf16_t*>(h));
+        else
+            hipLaunchKernelGGL(swiglu_backward_kernel<float>, dim3(grid), dim3(kThreads), 0, s,
+                               static_cast<const float*>(dh), guq, gu_scale, rows, nch, stride / nch,
+                               stride % nch, static_cast<float*>(d_gu), static_cast<float*>(h));
+    }
+    return launch_status("swiglu_backward_kernel");
+}
+
+}  // namespace moe

@@ -47,22 +47,28 @@ class MoELayer:
             self.xq = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=d)
             self.x_scale = torch.empty((T, H // 128), dtype=torch.float32, device=d)
 
-    def forward(self, x, logits, w13, w2, bias=None, w13_scale=None, w2_scale=None):
+    def forward(self, x, logits, w13, w2, bias=None, w13_scale=None, w2_scale=None, codes=None):
         """y [T, H] for x [T, H] and router logits [T, E] (fp32).  The result is
         the layer's own output buffer: the next call overwrites it, so clone it
-        to keep it."""
+        to keep it.  codes (fp8_act only): x already as (e4m3 codes, 1x128
+        scales), as rmsnorm(quantize=True) writes them; the quantise step is
+        then left out and x itself is not read (it may be None)."""
+        if codes is not None and not self.fp8_act:
+            raise ValueError("codes are the input of a layer with fp8 activations")
         B.route(logits, self.k, self.method, self.n_group, self.topk_group, bias, self.scaling,
                 self.renormalize, out=(self.ids, self.scales))
         B.permute(self.ids, self.E, self.n_shared, ws=self.ws,
                   out=(self.offsets, self.permuted_pair, self.unpermute))
         if self.fp8_act:
-            B.quantize_fp8(x, out=(self.xq, self.x_scale))
+            if codes is None:
+                codes = B.quantize_fp8(x, out=(self.xq, self.x_scale))
+            xq, x_scale = codes
             if self.fused:
-                B.expert_ffn_fp8_fused(self.xq, self.x_scale, self.offsets, self.permuted_pair,
+                B.expert_ffn_fp8_fused(xq, x_scale, self.offsets, self.permuted_pair,
                                        w13, w2, w13_scale, w2_scale, self.k, self.E,
                                        self.n_shared, split=self.split, out=self.fc2_out)
             else:
-                B.expert_ffn_fp8(self.xq, self.x_scale, self.offsets, self.permuted_pair, w13,
+                B.expert_ffn_fp8(xq, x_scale, self.offsets, self.permuted_pair, w13,
                                  w2, w13_scale, w2_scale, self.k, self.E, self.n_shared,
                                  ws=self.ws, out=self.fc2_out)
         elif self.fused:

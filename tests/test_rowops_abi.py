@@ -1,0 +1,212 @@
+"""The row operators without a GPU: their 64-bit forms against differences, and
+the host checks of every entry point (bad arguments are refused before
+anything is launched; the pointers here are never dereferenced)."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_layer_07_amd as moe
+import rowops_ref as ref
+from mixture_experts_layer_07_amd import binding
+
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+P = C.c_void_p(1 << 20)
+ODD = C.c_void_p((1 << 20) + 4)
+F32, BF16, FP8 = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def L():
+    import os
+    if not os.path.exists(binding.LIB_PATH):
+        from mixture_experts_layer_07_amd import build
+        build.build(verbose=False)
+    return moe.lib()
+
+
+# ------------------------------------------------- formulas against differences
+def rnd(*shape, seed=0):
+    return torch.from_numpy(np.random.default_rng(seed).standard_normal(shape))
+
+
+def close(a, b, tol):
+    assert abs(a - b) <= tol * max(1.0, abs(b)), (a, b)
+
+
+def test_rmsnorm_formula():
+    z, w, dy, v, u = rnd(5, 24), 1 + 0.1 * rnd(24, seed=1), rnd(5, 24, seed=2), rnd(5, 24, seed=3), rnd(24, seed=4)
+    dz, dw, _, _ = ref.rmsnorm_backward(dy, z, w, 1e-3)
+    close(ref.differences(lambda a: (ref.rmsnorm(a, w, 1e-3) * dy).sum(), z, v, 1e-5), float((dz * v).sum()), 1e-8)
+    close(ref.differences(lambda a: (ref.rmsnorm(z, a, 1e-3) * dy).sum(), w, u, 1e-5), float((dw * u).sum()), 1e-8)
+    both, _, _, _ = ref.rmsnorm_backward(dy, z, w, 1e-3, v)
+    assert torch.allclose(both, dz + v, rtol=0, atol=1e-14)
+
+
+def test_finalize_formula():
+    T, k, H, sh = 6, 3, 8, 2
+    up = torch.randperm(T * k, generator=torch.Generator().manual_seed(0)).int()
+    fc2, sc, dy = rnd(T * (k + sh), H), rnd(T, k, seed=1), rnd(T, H, seed=2)
+    vf, vs = rnd(*fc2.shape, seed=3), rnd(T, k, seed=4)
+    # the weighted rows' gradient is dispatch of scaled dy; with scales 1 its transpose is dispatch_backward
+    df = ref.dispatch(dy, up, k, sh)
+    df[up.long()] *= sc.reshape(-1, 1)
+    close(ref.differences(lambda a: (ref.finalize(a, up, sc, sh) * dy).sum(), fc2, vf, 1e-4), float((df * vf).sum()), 1e-8)
+    ds = (fc2[up.long()].view(T, k, H) * dy[:, None]).sum(2)
+    close(ref.differences(lambda a: (ref.finalize(fc2, up, a, sh) * dy).sum(), sc, vs, 1e-4), float((ds * vs).sum()), 1e-8)
+    dx, _ = ref.dispatch_backward(fc2, up, k, sh)
+    close(ref.differences(lambda a: (ref.dispatch(a, up, k, sh) * fc2).sum(), dy, rnd(T, H, seed=5), 1e-4),
+          float((dx * rnd(T, H, seed=5)).sum()), 1e-8)
+    assert torch.allclose(dx, ref.finalize(fc2, up, torch.ones(T, k), sh), rtol=1e-14, atol=1e-14)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("method", range(7))
+def test_route_formula(method, renorm):
+    T, E, k = 7, 11, 4
+    l, ds, v = rnd(T, E), rnd(T, k, seed=1), rnd(T, E, seed=2)
+    ids = l.topk(k, 1).indices.int()
+    d, size = ref.route_backward(l, ids, ds, method, 2.5, renorm)
+    f = lambda a: (ref.route_scales(a, ids, method, 2.5, renorm) * ds).sum()  # noqa: E731
+    close(ref.differences(f, l, v, 1e-5), float((d * v).sum()), 1e-8)
+    assert (d.abs() <= size * (1 + 1e-12)).all()
+
+
+def test_swiglu_formula():
+    gu, dh, v = rnd(5, 32), rnd(5, 16, seed=1), rnd(5, 32, seed=2)
+    d, size = ref.swiglu_backward(dh, gu)
+    close(ref.differences(lambda a: (ref.swiglu(a) * dh).sum(), gu, v, 1e-5), float((d * v).sum()), 1e-8)
+    assert (d.abs() <= size * (1 + 1e-12)).all()
+
+
+# ------------------------------------------------------------------- refusals
+def test_rmsnorm_validation(L):
+    def f(x=P, r=None, w=P, dt=BF16, T=4, H=256, eps=1e-6, total=None, y=P, q=None, s=None):
+        return L.moe_rmsnorm(x, r, w, dt, T, H, eps, total, y, q, s, None)
+
+    Q = C.c_void_p(1 << 21)
+    assert f(T=-1) == INVALID and f(H=0) == INVALID and f(dt=FP8) == INVALID and f(dt=7) == INVALID
+    assert f(H=100) == UNSUPPORTED                          # H % 8
+    assert f(H=16392) == UNSUPPORTED and "16384" in binding.last_error()
+    assert f(T=(1 << 30) + 1) == UNSUPPORTED
+    assert f(H=264, q=P, s=P) == UNSUPPORTED                # codes need H % 128
+    for eps in (0.0, -1e-6, float("inf"), float("nan")):
+        assert f(eps=eps) == INVALID
+    assert f(x=None) == INVALID and f(w=None) == INVALID
+    assert f(r=P) == INVALID and f(total=P) == INVALID      # residual and total together
+    assert f(q=P) == INVALID and f(s=P) == INVALID          # codes and scales together
+    assert f(y=None) == INVALID                             # nothing to write
+    assert f(r=P, total=Q, y=Q) == INVALID                  # two outputs, one buffer
+    for name in ("x", "r", "w", "total", "y", "q"):
+        a = dict(x=P, r=P, w=P, total=Q, y=P, q=P, s=P)
+        a[name] = ODD
+        assert f(**a) == INVALID and "aligned" in binding.last_error()
+    assert f(x=None, w=None, y=None, T=0) == OK
+
+
+def test_rmsnorm_backward_validation(L):
+    def f(dy=P, z=P, w=P, d=None, dt=BF16, T=4, H=256, eps=1e-6, dz=P, dw=P, ws=P, n=1 << 30):
+        return L.moe_rmsnorm_backward(dy, z, w, d, dt, T, H, eps, dz, dw, ws, n, None)
+
+    assert f(T=-1) == INVALID and f(H=0) == INVALID and f(dt=FP8) == INVALID and f(eps=0.0) == INVALID
+    assert f(H=100) == UNSUPPORTED and f(H=16392) == UNSUPPORTED
+    for name in ("dy", "z", "w", "dz", "dw"):
+        assert f(**{name: None}) == INVALID
+    for name in ("dy", "z", "w", "d", "dz", "ws"):
+        assert f(**{name: ODD}) == INVALID
+    assert f(ws=None) == WORKSPACE
+    need = L.moe_rmsnorm_backward_workspace_size(4, 256)
+    assert need > 0 and f(n=need - 1) == WORKSPACE
+    assert f(T=0, dw=None) == INVALID
+    size = L.moe_rmsnorm_backward_workspace_size
+    assert size(0, 256) == 0 and size(-1, 256) == 0 and size(4, 100) == 0
+    assert size(1 << 30, 16384) == size(1 << 20, 16384)     # bounded: not a row for each token
+
+
+def test_dispatch_validation(L):
+    def f(x=P, xs=None, dt=BF16, T=4, H=256, k=2, sh=0, up=P, rows=P, rs=None):
+        return L.moe_dispatch(x, xs, dt, T, H, k, sh, up, rows, rs, None)
+
+    assert f(T=-1) == INVALID and f(k=0) == INVALID and f(sh=-1) == INVALID and f(sh=65) == INVALID
+    assert f(k=9) == UNSUPPORTED and f(H=100) == UNSUPPORTED and f(dt=5) == INVALID and f(H=0) == INVALID
+    assert f(dt=FP8, H=264, xs=P, rs=P) == UNSUPPORTED
+    assert f(dt=FP8) == INVALID and f(dt=FP8, xs=P) == INVALID and f(xs=P, rs=P) == INVALID
+    assert f(x=None) == INVALID and f(up=None) == INVALID and f(rows=None) == INVALID
+    assert f(x=ODD) == INVALID and f(rows=ODD) == INVALID
+    assert f(T=1 << 29, k=4) == UNSUPPORTED
+    assert f(T=0, x=None, up=None, rows=None) == OK
+
+    def g(d=P, dt=BF16, up=P, T=4, k=2, H=256, sh=0, dx=P, dxt=BF16):
+        return L.moe_dispatch_backward(d, dt, up, T, k, H, sh, dx, dxt, None)
+
+    assert g(dt=FP8) == INVALID and g(dxt=FP8) == INVALID and g(k=9) == UNSUPPORTED and g(H=4) == UNSUPPORTED
+    assert g(d=None) == INVALID and g(up=None) == INVALID and g(dx=None) == INVALID
+    assert g(d=ODD) == INVALID and g(dx=ODD) == INVALID
+    assert g(T=0, d=None, up=None, dx=None) == OK
+
+
+def test_finalize_backward_validation(L):
+    def f(dy=P, dyt=BF16, r=P, dt=BF16, up=P, sc=P, T=4, k=2, H=256, sh=0, d=P, ds=P):
+        return L.moe_finalize_backward(dy, dyt, r, dt, up, sc, T, k, H, sh, d, ds, None)
+
+    assert f(T=-1) == INVALID and f(dyt=FP8) == INVALID and f(dt=FP8) == INVALID
+    assert f(k=9) == UNSUPPORTED and f(H=12) == UNSUPPORTED and f(T=1 << 29, k=4) == UNSUPPORTED
+    for name in ("dy", "r", "up", "sc", "d", "ds"):
+        assert f(**{name: None}) == INVALID
+    for name in ("dy", "r", "d"):
+        assert f(**{name: ODD}) == INVALID
+    assert f(T=0, dy=None, r=None, up=None, sc=None, d=None, ds=None) == OK
+
+
+def test_route_backward_validation(L):
+    def f(l=P, i=P, d=P, T=4, E=16, method=0, k=2, sc=1.0, flags=0, out=P):
+        return L.moe_route_backward(l, i, d, T, E, method, k, sc, flags, out, None)
+
+    assert f(T=-1) == INVALID and f(k=0) == INVALID and f(k=17) == INVALID and f(E=0) == INVALID
+    assert f(E=300) == UNSUPPORTED and f(E=64, k=9) == UNSUPPORTED
+    assert f(method=7) == UNSUPPORTED and f(method=8) == UNSUPPORTED
+    assert f(method=9) == INVALID and f(method=-1) == INVALID and f(flags=2) == INVALID
+    assert f(sc=float("nan")) == INVALID
+    for name in ("l", "i", "d", "out"):
+        assert f(**{name: None}) == INVALID
+    assert f(out=ODD) == INVALID
+    assert f(T=0, l=None, i=None, d=None, out=None) == OK
+
+
+def test_swiglu_validation(L):
+    def f(gu=P, dt=BF16, rows=4, I=256, h=P, hq=None, hs=None, q=None, qs=None):
+        return L.moe_swiglu(gu, dt, rows, I, h, hq, hs, q, qs, None)
+
+    assert f(rows=-1) == INVALID and f(I=0) == INVALID and f(dt=FP8) == INVALID and f(gu=None) == INVALID
+    assert f(I=12) == UNSUPPORTED and f(I=264, q=P, qs=P) == UNSUPPORTED and f(I=264, hq=P, hs=P) == UNSUPPORTED
+    assert f(rows=(1 << 30) + 1) == UNSUPPORTED and f(I=(1 << 29) + 128) == UNSUPPORTED
+    assert f(h=None) == INVALID
+    assert f(hq=P) == INVALID and f(hs=P) == INVALID and f(q=P) == INVALID and f(qs=P) == INVALID
+    assert f(gu=ODD) == INVALID and f(h=ODD) == INVALID
+    assert f(hq=ODD, hs=P) == INVALID and f(q=ODD, qs=P) == INVALID
+    assert f(rows=0, gu=None, h=None) == OK
+
+    def g(dh=P, dt=BF16, q=P, qs=P, rows=4, I=256, d=P, h=None):
+        return L.moe_swiglu_backward(dh, dt, q, qs, rows, I, d, h, None)
+
+    assert g(rows=-1) == INVALID and g(I=0) == INVALID and g(dt=FP8) == INVALID
+    assert g(I=264) == UNSUPPORTED
+    for name in ("dh", "q", "qs", "d"):
+        assert g(**{name: None}) == INVALID
+    for name in ("dh", "q", "d", "h"):
+        assert g(**{name: ODD}) == INVALID
+    assert g(rows=0, dh=None, q=None, qs=None, d=None) == OK
+
+
+def test_binding_refuses_host_tensors():
+    x, w = torch.zeros(4, 256), torch.ones(256)
+    i = torch.zeros(8, dtype=torch.int32)
+    calls = [lambda: moe.rmsnorm(x, w), lambda: moe.rmsnorm_backward(x, x, w),
+             lambda: moe.dispatch(x, i, 2), lambda: moe.dispatch_backward(x, i, 2),
+             lambda: moe.finalize_backward(x, x, i, torch.zeros(4, 2)),
+             lambda: moe.route_backward(x, i.view(4, 2), torch.zeros(4, 2), 0),
+             lambda: moe.swiglu(x), lambda: moe.swiglu_backward(x, x, x)]
+    for call in calls:
+        with pytest.raises(ValueError, match="must be a GPU tensor"):
+            call()
