@@ -330,10 +330,10 @@ moe_status moe_expert_ffn_fp8_fused(const uint8_t* xq, const float* x_scale, int
  * The row operators below share these rules beyond the ones at the top:
  *  - dt is MOE_F32 or MOE_BF16; sums, norms and softmax statistics are fp32 or
  *    wider and every output is rounded once, to its own type.
- *  - Device pointers of [rows, columns] arrays are 16-byte aligned
- *    (MOE_ERR_INVALID_ARG otherwise); int32 and fp32 [T, k], [rows, cols/128]
- *    and [H] arrays of `unpermute`, scales and `dweight` need only their
- *    element's alignment.
+ *  - Device pointers of arrays whose last dimension is H, I or 2I (weight and
+ *    dweight among them), d_logits and the workspace are 16-byte aligned
+ *    (MOE_ERR_INVALID_ARG otherwise); the others need only their element's
+ *    alignment.
  *  - An output may not overlap an input or another output except where the
  *    call says so.
  *  - Rows are independent: a NaN or infinity in one row changes no other row

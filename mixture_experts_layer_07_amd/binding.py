@@ -1,20 +1,22 @@
-"""ctypes binding of libmoe.so (include/moe.h).
+"""Binding of libmoe.so (include/moe.h).
 
 Argument marshalling only: tensors are checked for device/dtype/shape and
 handed over as raw pointers together with torch's current HIP stream; every
-step of the layer runs in the library's kernels.  There is no fallback: if the
-library is missing or a call fails, an exception says so.
+step of the layer runs in the library's kernels.  The checks and the calls
+themselves are native (csrc/marshal.cpp, _marshal.so), the rest is ctypes.
+There is no fallback: if a library is missing or a call fails, an exception
+says so.
 """
 from __future__ import annotations
 
 import ctypes as C
 import os
-from typing import Optional
 
 import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
+MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
 
 MOE_OK = 0
 F32, BF16, FP8_E4M3 = 0, 1, 2
@@ -29,6 +31,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 
 _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3}
 _lib = None
+_marshal = None
 
 
 class MoeError(RuntimeError):
@@ -39,11 +42,12 @@ class MoeError(RuntimeError):
 
 def lib():
     """The loaded libmoe.so with argument types set (raises if not built)."""
-    global _lib
+    global _lib, _marshal, _dev
     if _lib is None:
-        if not os.path.exists(LIB_PATH):
-            raise RuntimeError(f"{LIB_PATH} is not built; run "
-                               "`python -m mixture_experts_layer_07_amd.build`")
+        for path in (LIB_PATH, MARSHAL_PATH):
+            if not os.path.exists(path):
+                raise RuntimeError(f"{path} is not built; run "
+                                   "`python -m mixture_experts_layer_07_amd.build`")
         L = C.CDLL(LIB_PATH)
         P, i, u, f, z = C.c_void_p, C.c_int, C.c_uint, C.c_float, C.c_size_t
         L.moe_route.argtypes = [P, i, i, i, i, i, i, P, f, u, P, P, P]
@@ -80,7 +84,9 @@ def lib():
                    "moe_route_backward", "moe_swiglu", "moe_swiglu_backward",
                    "moe_timing_enable", "moe_kernel_times"):
             getattr(L, fn).restype = C.c_int
-        _lib = L
+        from . import _marshal as native
+        native.setup(lambda fn: C.cast(getattr(L, fn), C.c_void_p).value, _failed, _refuse)
+        _lib, _marshal, _dev = L, native, native.check
     return _lib
 
 
@@ -92,46 +98,40 @@ def last_error() -> str:
     return lib().moe_last_error().decode()
 
 
+def _failed(fn: str, st: int):
+    raise MoeError(fn, st, last_error())
+
+
 def _check(fn: str, st: int):
     if st != MOE_OK:
-        raise MoeError(fn, st, last_error())
-
-
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else C.c_void_p(t.data_ptr())
-
-
-def _stream(device) -> C.c_void_p:
-    return C.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+        _failed(fn, st)
 
 
 def _call(fn: str, device, *args):
     """Calls library entry `fn` with `device` current and its current stream
     appended; tensor arguments become device pointers and must all live on
     `device` (the kernels run on the current device)."""
-    device = torch.device(device)
-    conv = []
-    for a in args:
-        if isinstance(a, torch.Tensor):
-            if a.device != device:
-                raise ValueError(f"{fn}: a tensor on {a.device}, expected {device}")
-            a = _ptr(a)
-        conv.append(a)
-    with torch.cuda.device(device):
-        st = getattr(lib(), fn)(*conv, _stream(device))
-    _check(fn, st)
+    if _lib is None:
+        lib()
+    _marshal.call(fn, device if isinstance(device, torch.device) else torch.device(device), *args)
 
 
-def _dev(t: torch.Tensor, name: str, dtype=None, shape=None):
+def _refuse(t, name, dtype, shape):
+    """Says what _dev found."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    return t
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _dev(t: torch.Tensor, name: str, dtype=None, shape=None):
+    """t if it is a contiguous GPU tensor of that dtype (or one of a tuple of
+    dtypes) and shape.  lib() puts the native form in this one's place."""
+    lib()
+    return _marshal.check(t, name, dtype, shape)
 
 
 def dtype_code(dt: torch.dtype) -> int:

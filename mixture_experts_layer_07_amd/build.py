@@ -1,5 +1,6 @@
-"""Build libmoe.so (the gfx950 HIP library behind include/moe.h) and the
-benchmark's calibration library libmoe_calib.so in-tree.
+"""Build libmoe.so (the gfx950 HIP library behind include/moe.h), the binding's
+native half _marshal.so and the benchmark's calibration library libmoe_calib.so
+in-tree.
 
     python -m mixture_experts_layer_07_amd.build
 """
@@ -15,6 +16,8 @@ SOURCES = ["api.hip", "route.hip", "permute.hip", "ffn.hip", "fused.hip", "final
            "quant.hip", "noalloc.hip", "norm.hip", "dispatch.hip", "swiglu.hip", "route_backward.hip"]
 CALIB_SOURCE = "calib.hip"
 CALIB_LIB = os.path.join(HERE, "libmoe_calib.so")
+MARSHAL_SOURCE = "marshal.cpp"
+MARSHAL_LIB = os.path.join(HERE, "_marshal.so")
 ARCH = os.environ.get("MOE_OFFLOAD_ARCH", "gfx950")
 
 HIPCC_FLAGS = [
@@ -27,6 +30,29 @@ HIPCC_FLAGS = [
 
 def _hipcc():
     return os.path.join(os.environ.get("ROCM_PATH", "/opt/rocm"), "bin", "hipcc")
+
+
+def build_marshal(verbose: bool = True) -> str:
+    """The host-only extension module behind binding.py, against torch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    tmp = MARSHAL_LIB + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch.compiled_with_cxx11_abi(),
+           *["-isystem" + d for d in include_paths()], "-I" + sysconfig.get_paths()["include"],
+           os.path.join(CSRC, MARSHAL_SOURCE), "-o", tmp,
+           "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n%s\n%s" % (" ".join(cmd), r.stdout + r.stderr))
+    os.replace(tmp, MARSHAL_LIB)
+    if verbose:
+        print("built", MARSHAL_LIB, flush=True)
+    return MARSHAL_LIB
 
 
 def build(verbose: bool = True, jobs: int = 5) -> str:
@@ -55,6 +81,7 @@ def build(verbose: bool = True, jobs: int = 5) -> str:
     os.replace(tmp, LIB)
     if verbose:
         print("built", LIB, flush=True)
+    build_marshal(verbose)
     # the benchmark's HBM read calibration kernel, a library of its own
     obj = compile_one(CALIB_SOURCE)
     tmp = CALIB_LIB + ".tmp%d" % os.getpid()

@@ -476,7 +476,7 @@ moe_status moe_rmsnorm_backward(const void* dy, const void* z, const void* weigh
     if (T > 0) {
         if (!dy || !z || !weight || !dz)
             return set_error(MOE_ERR_INVALID_ARG, "dy, z, weight and dz must be non-null");
-        if (!aligned16({dy, z, weight, dtotal, dz, ws})) return misaligned();
+        if (!aligned16({dy, z, weight, dtotal, dz, dweight, ws})) return misaligned();
         const size_t need = rmsnorm_backward_scratch_bytes(T, H);
         if (!ws || ws_bytes < need)
             return set_error(MOE_ERR_WORKSPACE, "rmsnorm_backward needs %zu workspace bytes (got %zu)", need,

@@ -14,8 +14,9 @@
 namespace moe {
 namespace {
 
-constexpr int kMaxWaves = 8;
+constexpr int kMaxWaves = 16;
 constexpr int kPartials = 512;  // most partial rows of dweight (sets the workspace's size)
+constexpr int kFewRows = 512;   // up to here the forward pass gives a row one chunk a thread
 
 // Sums of N values over the row's threads: one wave, or the workgroup through
 // LDS.  `buf` alternates between two halves on consecutive calls, so one
@@ -43,8 +44,8 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*s)[kMaxWaves][N],
 }
 
 // No __restrict__: total and y may be x or residual.
-template <class T, int NV, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 512) void rmsnorm_kernel(const T* x, const T* residual, const T* weight,
+template <class T, int NV, bool WAVE, bool NT>
+__global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const T* x, const T* residual, const T* weight,
                                                        int rows, int H, float eps, T* total, T* y,
                                                        uint8_t* yq, float* y_scale)
 {
@@ -66,8 +67,8 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void rmsnorm_kernel(const T* x, c
             b[i].zero();
             w[i].zero();
             if (c < nch) {
-                a[i].load(x + r0 + 8 * c);
-                if (residual) b[i].load(residual + r0 + 8 * c);
+                a[i].template load<NT>(x + r0 + 8 * c);
+                if (residual) b[i].template load<NT>(residual + r0 + 8 * c);
                 w[i].load(weight + 8 * c);
             }
         }
@@ -80,7 +81,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void rmsnorm_kernel(const T* x, c
                 for (int e = 0; e < 8; ++e) z[e] = a[i][e] + b[i][e];
                 a[i].set(z);  // the norm is taken of the stored sum
                 const int c = tid + i * stride;
-                if (c < nch) a[i].store(total + r0 + 8 * c);
+                if (c < nch) a[i].template store<NT>(total + r0 + 8 * c);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[0] += a[i][e] * a[i][e];
@@ -96,7 +97,7 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void rmsnorm_kernel(const T* x, c
             if (y && c < nch) {
                 Raw8<T> o;
                 o.set(v);
-                o.store(y + r0 + 8 * c);
+                o.template store<NT>(y + r0 + 8 * c);
             }
             if (yq) {  // H is a multiple of 128: the 16 lanes of a block are in or out together
                 const float s = max16(absmax8(v)) / 448.0f;
@@ -110,14 +111,16 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void rmsnorm_kernel(const T* x, c
 }
 
 // Workgroup b takes rows b, b + grid, ... and adds its rows' dy z c in
-// registers; its sum is one row of `part`.
-template <class T, int NV, bool WAVE>
-__global__ __launch_bounds__(WAVE ? 256 : 512) void rmsnorm_backward_kernel(
+// registers; its sum is one row of `part`.  The next row's loads are issued
+// before the current row's reduction where the registers hold both rows.
+template <class T, int NV, bool WAVE, bool NT>
+__global__ __launch_bounds__(WAVE ? 1024 : 512) void rmsnorm_backward_kernel(
     const T* dy, const T* z, const T* weight, const T* dtotal, int rows, int H, float eps, T* dz,
     float* __restrict__ part)
 {
+    constexpr bool kAhead = WAVE && NV == 1;
     __shared__ float s_sum[2][kMaxWaves][2];
-    __shared__ float s_dw[WAVE ? 4 : 1][WAVE ? 512 * NV : 1];
+    __shared__ float s_dw[WAVE ? 8 : 1][WAVE ? 512 * NV : 1];
     int buf = 0;
     const int wave = threadIdx.x >> 6;
     const int tid = WAVE ? (threadIdx.x & 63) : threadIdx.x;
@@ -125,6 +128,9 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void rmsnorm_backward_kernel(
     const int per = WAVE ? (blockDim.x >> 6) : 1;
     const int nch = H >> 3;
     const float inv = 1.0f / (float)H;
+    struct Row {
+        Raw8<T> z[NV], g[NV], d[NV];
+    };
     Raw8<T> w[NV];
     float dw[NV][8];
 #pragma unroll
@@ -135,28 +141,35 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void rmsnorm_backward_kernel(
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
     }
-    for (long row = (long)blockIdx.x * per + (WAVE ? wave : 0); row < rows; row += (long)gridDim.x * per) {
+    const long step = (long)gridDim.x * per;
+    auto fetch = [&](Row& r, long row) {
         const size_t r0 = (size_t)row * H;
-        Raw8<T> a[NV], g[NV], d[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * stride;
-            a[i].zero();
-            g[i].zero();
-            d[i].zero();
-            if (c < nch) {
-                a[i].load(z + r0 + 8 * c);
-                g[i].load(dy + r0 + 8 * c);
-                if (dtotal) d[i].load(dtotal + r0 + 8 * c);
+            r.z[i].zero();
+            r.g[i].zero();
+            r.d[i].zero();
+            if (c < nch && row < rows) {
+                r.z[i].template load<NT>(z + r0 + 8 * c);
+                r.g[i].template load<NT>(dy + r0 + 8 * c);
+                if (dtotal) r.d[i].template load<NT>(dtotal + r0 + 8 * c);
             }
         }
+    };
+    Row cur, next;
+    long row = (long)blockIdx.x * per + (WAVE ? wave : 0);
+    if constexpr (kAhead) fetch(cur, row);
+    for (; row < rows; row += step) {
+        if constexpr (kAhead) fetch(next, row + step);
+        else fetch(cur, row);
         float sum[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                sum[0] += a[i][e] * a[i][e];
-                sum[1] += g[i][e] * w[i][e] * a[i][e];
+                sum[0] += cur.z[i][e] * cur.z[i][e];
+                sum[1] += cur.g[i][e] * w[i][e] * cur.z[i][e];
             }
         row_sum<WAVE, 2>(sum, s_sum, buf);
         const float cn = rsqrtf(sum[0] * inv + eps);
@@ -167,27 +180,38 @@ __global__ __launch_bounds__(WAVE ? 256 : 512) void rmsnorm_backward_kernel(
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[e] = cn * (g[i][e] * w[i][e]) - a[i][e] * m + d[i][e];
-                dw[i][e] += g[i][e] * (a[i][e] * cn);
+                v[e] = cn * (cur.g[i][e] * w[i][e]) - cur.z[i][e] * m + cur.d[i][e];
+                dw[i][e] += cur.g[i][e] * (cur.z[i][e] * cn);
             }
             if (c < nch) {
                 Raw8<T> o;
                 o.set(v);
-                o.store(dz + r0 + 8 * c);
+                o.template store<NT>(dz + (size_t)row * H + 8 * c);
             }
         }
+        if constexpr (kAhead) cur = next;
     }
     float* out = part + (size_t)blockIdx.x * H;
-    if constexpr (WAVE) {  // the four waves' sums, in order
+    if constexpr (WAVE) {  // the waves' sums, added in order, eight waves at a time
+        float v[4] = {0.f, 0.f, 0.f, 0.f};  // a 256-thread workgroup has up to 4 columns a thread
+        for (int k0 = 0; k0 < per; k0 += 8) {
+            if (wave >= k0 && wave < k0 + 8) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+                for (int i = 0; i < NV; ++i) store8_f32(&s_dw[wave - k0][8 * (tid + 64 * i)], dw[i]);
+            }
+            __syncthreads();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s_dw[wave][8 * (tid + 64 * i) + e] = dw[i][e];
-        __syncthreads();
-        for (int h = threadIdx.x; h < H; h += blockDim.x) {
-            float v = 0.0f;
-            for (int k = 0; k < per; ++k) v += s_dw[k][h];
-            out[h] = v;
+            for (int q = 0; q < 4; ++q) {
+                const int h = threadIdx.x + q * blockDim.x;
+                if (h < H)
+                    for (int k = 0; k < min(8, per - k0); ++k) v[q] += s_dw[k][h];
+            }
+            __syncthreads();
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int h = threadIdx.x + q * blockDim.x;
+            if (h < H) out[h] = v[q];
         }
     } else {
 #pragma unroll
@@ -226,75 +250,93 @@ __global__ __launch_bounds__(1024) void rmsnorm_dweight_kernel(const float* __re
 struct Shape {
     bool wave;    // a wave a row, else a workgroup
     int threads;  // of a workgroup
-    int nv;       // chunks a thread: 1, 2 or 4
+    int nv;       // chunks a thread
     int per;      // rows a workgroup takes at a time
+    int grid;
 };
 
-Shape shape_of(int H)
+Shape forward_shape(int T, int H)
 {
     const int nch = H / 8;
     Shape s;
     s.wave = nch <= 256;
-    s.threads = s.wave ? 256 : nch <= 1024 ? 256 : 512;
-    const int each = (nch + (s.wave ? 64 : s.threads) - 1) / (s.wave ? 64 : s.threads);
-    s.nv = each <= 1 ? 1 : each <= 2 ? 2 : 4;
-    s.per = s.wave ? 4 : 1;
+    if (s.wave) {
+        s.threads = 256;
+        s.nv = nch <= 64 ? 1 : nch <= 128 ? 2 : 4;
+        s.per = 4;
+    } else {
+        s.nv = T <= kFewRows && nch <= 1024 ? 1 : 2;
+        s.threads = (nch + 64 * s.nv - 1) / (64 * s.nv) * 64;
+        s.per = 1;
+    }
+    s.grid = std::min((T + s.per - 1) / s.per, 1 << 20);
+    return s;
+}
+
+Shape backward_shape(int T, int H)
+{
+    const int nch = H / 8;
+    Shape s;
+    s.wave = nch <= 128;
+    if (s.wave) {
+        s.threads = T <= 64 ? 1024 : 256;
+        s.nv = nch <= 64 ? 1 : 2;
+        s.per = s.threads / 64;
+    } else {
+        s.nv = 4;
+        s.threads = (nch + 255) / 256 * 64;
+        s.per = 1;
+    }
+    // up to four rows one after the other cost less than the second launch that sums the partial rows
+    s.grid = T <= 4 * s.per ? 1 : std::min((T + s.per - 1) / s.per, kPartials);
     return s;
 }
 
 template <class T, int NV, bool WAVE>
-void launch_fwd(const Shape& sh, int grid, const void* x, const void* residual, const void* weight, int T_,
+void launch_fwd(const Shape& sh, const void* x, const void* residual, const void* weight, int T_,
                 int H, float eps, void* total, void* y, uint8_t* yq, float* ys, hipStream_t s)
 {
-    hipLaunchKernelGGL((rmsnorm_kernel<T, NV, WAVE>), dim3(grid), dim3(sh.threads), 0, s,
+    const bool nt = (long)T_ * H * (long)sizeof(T) * (residual ? 4 : 2) > kStream;
+    auto* kernel = nt ? rmsnorm_kernel<T, NV, WAVE, true> : rmsnorm_kernel<T, NV, WAVE, false>;
+    hipLaunchKernelGGL(kernel, dim3(sh.grid), dim3(sh.threads), 0, s,
                        static_cast<const T*>(x), static_cast<const T*>(residual),
                        static_cast<const T*>(weight), T_, H, eps, static_cast<T*>(total),
                        static_cast<T*>(y), yq, ys);
 }
 
 template <class T, int NV, bool WAVE>
-void launch_bwd(const Shape& sh, int grid, const void* dy, const void* z, const void* weight,
+void launch_bwd(const Shape& sh, const void* dy, const void* z, const void* weight,
                 const void* dtotal, int T_, int H, float eps, void* dz, float* part, hipStream_t s)
 {
-    hipLaunchKernelGGL((rmsnorm_backward_kernel<T, NV, WAVE>), dim3(grid), dim3(sh.threads), 0, s,
+    const bool nt = (long)T_ * H * (long)sizeof(T) * (dtotal ? 4 : 3) > kStream;
+    auto* kernel = nt ? rmsnorm_backward_kernel<T, NV, WAVE, true> : rmsnorm_backward_kernel<T, NV, WAVE, false>;
+    hipLaunchKernelGGL(kernel, dim3(sh.grid), dim3(sh.threads), 0, s,
                        static_cast<const T*>(dy), static_cast<const T*>(z), static_cast<const T*>(weight),
                        static_cast<const T*>(dtotal), T_, H, eps, static_cast<T*>(dz), part);
 }
 
-// Calls f with T, NV and WAVE as template arguments.
-#define MOE_NORM_SHAPE(T, f, ...)                                                       \
-    do {                                                                                \
-        if (sh.wave) {                                                                  \
-            if (sh.nv == 1) f<T, 1, true>(__VA_ARGS__);                                 \
-            else if (sh.nv == 2) f<T, 2, true>(__VA_ARGS__);                            \
-            else f<T, 4, true>(__VA_ARGS__);                                            \
-        } else {                                                                        \
-            if (sh.nv == 2) f<T, 2, false>(__VA_ARGS__);                                \
-            else f<T, 4, false>(__VA_ARGS__);                                           \
-        }                                                                               \
-    } while (0)
-
-int partials(int T, int H)
-{
-    const Shape sh = shape_of(H);
-    return std::min((T + sh.per - 1) / sh.per, kPartials);
-}
-
 }  // namespace
 
-size_t rmsnorm_backward_scratch_bytes(int T, int H) { return (size_t)partials(T, H) * H * sizeof(float); }
+size_t rmsnorm_backward_scratch_bytes(int T, int H)
+{
+    return (size_t)backward_shape(T, H).grid * H * sizeof(float);
+}
 
 moe_status launch_rmsnorm(const void* x, const void* residual, const void* weight, int dt, int T, int H,
                           float eps, void* total, void* y, uint8_t* yq, float* y_scale, hipStream_t s)
 {
-    const Shape sh = shape_of(H);
-    const int grid = std::min((T + sh.per - 1) / sh.per, 1 << 20);
+    const Shape sh = forward_shape(T, H);
     {
         TimedLaunch tl(MOE_KID_RMSNORM, s);
-        if (dt == MOE_BF16)
-            MOE_NORM_SHAPE(bf16_t, launch_fwd, sh, grid, x, residual, weight, T, H, eps, total, y, yq, y_scale, s);
-        else
-            MOE_NORM_SHAPE(float, launch_fwd, sh, grid, x, residual, weight, T, H, eps, total, y, yq, y_scale, s);
+        auto go = [&](auto type) {
+            using V = decltype(type);
+            auto* f = !sh.wave ? (sh.nv == 1 ? launch_fwd<V, 1, false> : launch_fwd<V, 2, false>)
+                      : sh.nv == 1 ? launch_fwd<V, 1, true>
+                      : sh.nv == 2 ? launch_fwd<V, 2, true> : launch_fwd<V, 4, true>;
+            f(sh, x, residual, weight, T, H, eps, total, y, yq, y_scale, s);
+        };
+        if (dt == MOE_BF16) go(bf16_t{});
+        else go(float{});
     }
     return launch_status("rmsnorm_kernel");
 }
@@ -303,19 +345,24 @@ moe_status launch_rmsnorm_backward(const void* dy, const void* z, const void* we
                                    int dt, int T, int H, float eps, void* dz, float* dweight, void* ws,
                                    hipStream_t s)
 {
-    const int n = T ? partials(T, H) : 0;
-    float* part = static_cast<float*>(ws);
-    if (n > 0) {
-        const Shape sh = shape_of(H);
+    const Shape sh = backward_shape(T, H);
+    // a single workgroup's sum is the answer
+    float* part = T > 0 && sh.grid == 1 ? dweight : static_cast<float*>(ws);
+    if (T > 0) {
         TimedLaunch tl(MOE_KID_RMSNORM_BWD, s);
-        if (dt == MOE_BF16)
-            MOE_NORM_SHAPE(bf16_t, launch_bwd, sh, n, dy, z, weight, dtotal, T, H, eps, dz, part, s);
-        else
-            MOE_NORM_SHAPE(float, launch_bwd, sh, n, dy, z, weight, dtotal, T, H, eps, dz, part, s);
+        auto go = [&](auto type) {
+            using V = decltype(type);
+            auto* f = !sh.wave ? launch_bwd<V, 4, false>
+                      : sh.nv == 1 ? launch_bwd<V, 1, true> : launch_bwd<V, 2, true>;
+            f(sh, dy, z, weight, dtotal, T, H, eps, dz, part, s);
+        };
+        if (dt == MOE_BF16) go(bf16_t{});
+        else go(float{});
     }
-    {
+    if (part != dweight) {
         TimedLaunch tl(MOE_KID_RMSNORM_DWEIGHT, s);
-        hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((H + 31) / 32), dim3(1024), 0, s, part, n, H, dweight);
+        hipLaunchKernelGGL(rmsnorm_dweight_kernel, dim3((H + 31) / 32), dim3(1024), 0, s, part, T ? sh.grid : 0, H,
+                           dweight);
     }
     return launch_status("rmsnorm_backward_kernel");
 }

@@ -8,11 +8,13 @@
 // nothing.  Written so, nothing cancels where one weight is near 1, and one
 // renormalised weight alone has gradient exactly 0.
 //
-// Latency-bound: it writes T*E floats and reads little.  A workgroup owns
-// kTok tokens.  Eight lanes a token compute the kept experts' gradients in
-// fp64 (k exponentials a token); they go to a tile of the output in LDS, which
-// is then written as one contiguous run.  Plain softmax, where every logit has
-// a gradient, first takes each row's statistics, 8 lanes a row.
+// Latency-bound: it writes T*E floats and reads little.  A wave owns eight
+// tokens, eight lanes each: they compute the kept experts' gradients in fp64 (k
+// exponentials a token) and put them into a tile of the output in LDS, which is
+// then written as one contiguous run.  Plain softmax, where every logit has a
+// gradient, first reads the tile's logits as one run and takes each row's
+// statistics; the rows' walks start 8 columns apart so that the eight rows do
+// not meet in the same LDS banks.
 #include <algorithm>
 
 #include "rowops.h"
@@ -20,7 +22,8 @@
 namespace moe {
 namespace {
 
-constexpr int kTok = 32;      // tokens a 256-thread workgroup: 8 lanes each
+constexpr int kTok = 8;       // tokens a wave
+constexpr int kThreads = 64;  // a workgroup is one wave: its barriers cost nothing
 constexpr int kMaxGrid = 1 << 20;
 
 template <class V>
@@ -40,11 +43,26 @@ __device__ __forceinline__ V max8(V v)
     return fmax(v, __shfl_xor(v, 4, 64));
 }
 
-__global__ __launch_bounds__(256) void route_backward_kernel(const float* __restrict__ logits,
+// Calls f with the columns that lane j takes of its token's row: 8 q + j for q
+// from tl on, around the end.
+template <class F>
+__device__ __forceinline__ void walk(int E, int tl, int j, F f)
+{
+    const int n = (E + 7) >> 3;
+    int q = tl % n;
+#pragma unroll 4
+    for (int s = 0; s < n; ++s) {
+        const int i = 8 * q + j;
+        if (i < E) f(i);
+        q = q + 1 == n ? 0 : q + 1;
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void route_backward_kernel(const float* __restrict__ logits,
                                                              const int32_t* __restrict__ ids,
                                                              const float* __restrict__ d_scales, int T, int E,
                                                              int method, int k, float scaling, bool whole,
-                                                             float* __restrict__ d_logits)
+                                                             bool aligned, float* __restrict__ d_logits)
 {
     __shared__ __align__(16) float s_out[kTok * MOE_MAX_EXPERTS];
     const int lane = threadIdx.x & 63;
@@ -58,13 +76,29 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
         double d = 0.0, l = 0.0;
         if (tl < nt && j < k) {
             e = ids[t * k + j];
-            if ((unsigned)e >= (unsigned)E) e = -1;  // a dropped pair
-            if (e >= 0) {
-                d = d_scales[t * k + j];
-                l = logits[t * E + e];
-            }
+            d = d_scales[t * k + j];
         }
-        if (whole) {  // every expert once: the first of several pairs takes the others' gradients
+        float* row = s_out + tl * E;
+        // the tile: zeros, or its logits (t0 * E is a multiple of 4, so a run starts on a 16-byte boundary)
+        const int n = nt * E;
+        const float* in = logits + t0 * E;
+        if (!whole || aligned) {
+#pragma unroll 4
+            for (int i = threadIdx.x; i < (n >> 2); i += kThreads)
+                reinterpret_cast<float4*>(s_out)[i] =
+                    whole ? reinterpret_cast<const float4*>(in)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = (n & ~3) + threadIdx.x; i < n; i += kThreads) s_out[i] = whole ? in[i] : 0.0f;
+        } else {
+            for (int i = threadIdx.x; i < n; i += kThreads) s_out[i] = in[i];
+        }
+        if ((unsigned)e >= (unsigned)E) {  // a dropped pair
+            e = -1;
+            d = 0.0;
+        }
+        if (!whole && e >= 0) l = logits[t * E + e];
+        double m = 0.0, rest = 0.0;  // maximum, and the sum of what is not kept
+        if (whole) {
+            // every expert once: the first of several pairs takes the others' gradients
             double sum = 0.0;
             bool first = true;
 #pragma unroll
@@ -78,22 +112,10 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
             }
             d = first ? sum : 0.0;
             e = first ? e : -1;
-        }
-        float* row = s_out + tl * E;
-        if (!whole) {
-            const int n4 = (nt * E + 3) >> 2;
-            for (int i = threadIdx.x; i < n4; i += 256)
-                reinterpret_cast<float4*>(s_out)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        double m = 0.0, rest = 0.0;  // maximum, and the sum of what is not kept
-        if (whole) {
+            __syncthreads();
+            if (e >= 0) l = row[e];
             float mx = -INFINITY;
-            if (tl < nt)
-                for (int i = j; i < E; i += 8) {
-                    const float v = logits[t * E + i];
-                    row[i] = v;
-                    mx = fmaxf(mx, v);
-                }
+            if (tl < nt) walk(E, tl, j, [&](int i) { mx = fmaxf(mx, row[i]); });
             mx = max8(mx);
             m = mx;
             __syncthreads();
@@ -101,11 +123,11 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
             __syncthreads();
             float z = 0.0f;
             if (tl < nt)
-                for (int i = j; i < E; i += 8) {
+                walk(E, tl, j, [&](int i) {
                     const float p = mx == -INFINITY ? 0.0f : expf(row[i] - mx);
                     row[i] = p;
                     z += p;
-                }
+                });
             rest = sum8((double)z);
         } else if (!sigm) {
             m = max8(e >= 0 ? l : (double)-INFINITY);
@@ -148,17 +170,15 @@ __global__ __launch_bounds__(256) void route_backward_kernel(const float* __rest
         __syncthreads();
         if (whole && tl < nt) {
             const float f = (float)(-mean * scaling);
-            for (int i = j; i < E; i += 8) row[i] *= f;
+            walk(E, tl, j, [&](int i) { row[i] *= f; });
         }
         if (whole) __syncthreads();
         if (e >= 0) row[e] = (float)both;
         __syncthreads();
-        // t0 is a multiple of 32, so the run starts on a 16-byte boundary
-        const int n = nt * E;
         float* out = d_logits + t0 * E;
-        for (int i = threadIdx.x; i < (n >> 2); i += 256)
+        for (int i = threadIdx.x; i < (n >> 2); i += kThreads)
             reinterpret_cast<float4*>(out)[i] = reinterpret_cast<const float4*>(s_out)[i];
-        for (int i = (n & ~3) + threadIdx.x; i < n; i += 256) out[i] = s_out[i];
+        for (int i = (n & ~3) + threadIdx.x; i < n; i += kThreads) out[i] = s_out[i];
         __syncthreads();
     }
 }
@@ -173,8 +193,8 @@ moe_status launch_route_backward(const float* logits, const int32_t* ids, const 
     const int grid = (int)std::min(((long)T + kTok - 1) / kTok, (long)kMaxGrid);
     {
         TimedLaunch tl(MOE_KID_ROUTE_BWD, s);
-        hipLaunchKernelGGL(route_backward_kernel, dim3(grid), dim3(256), 0, s, logits, ids, d_scales, T, E, method,
-                           k, scaling, whole, d_logits);
+        hipLaunchKernelGGL(route_backward_kernel, dim3(grid), dim3(kThreads), 0, s, logits, ids, d_scales, T, E, method,
+                           k, scaling, whole, (reinterpret_cast<uintptr_t>(logits) & 15) == 0, d_logits);
     }
     return launch_status("route_backward_kernel");
 }

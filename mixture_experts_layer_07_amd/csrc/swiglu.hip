@@ -15,7 +15,7 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 
 // e^-g: bf16 outputs keep 9 bits, so the product form of exp (relative error
 // below 2^-22 |g|) serves; fp32 outputs take the library's function.
@@ -33,7 +33,7 @@ __device__ __forceinline__ float sigmoid(float g)
     else return 1.0f / (1.0f + exp_neg<T>(g));
 }
 
-template <class T>
+template <class T, bool NT>
 __global__ __launch_bounds__(kThreads) void swiglu_kernel(const T* __restrict__ gu, int rows, int nch, int drow,
                                                           int dcol, T* __restrict__ h, uint8_t* __restrict__ hq,
                                                           float* __restrict__ h_scale, uint8_t* __restrict__ guq,
@@ -57,7 +57,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const T* __restrict__ 
         if (h) {
             Raw8<T> w;
             w.set(o);
-            w.store(h + h0);
+            w.template store<NT>(h + h0);
         }
         // 8-bit outputs: I is a multiple of 128, so 16 lanes share a row and a block
         if (hq) {
@@ -84,7 +84,7 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const T* __restrict__ 
 }
 
 // No __restrict__ on dh and h: they may be the same rows.
-template <class T>
+template <class T, bool NT>
 __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(const T* dh, const uint8_t* __restrict__ guq,
                                                                    const float* __restrict__ gu_scale, int rows,
                                                                    int nch, int drow, int dcol,
@@ -111,12 +111,12 @@ __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(const T* dh, 
         }
         Raw8<T> w;
         w.set(dg);
-        w.store(d_gu + g0);
+        w.template store<NT>(d_gu + g0);
         w.set(du);
-        w.store(d_gu + g0 + I);
+        w.template store<NT>(d_gu + g0 + I);
         if (h) {
             w.set(o);
-            w.store(h + h0);
+            w.template store<NT>(h + h0);
         }
         row += drow;
         col += dcol;
@@ -135,39 +135,47 @@ int grid_of(int rows, int nch)
 
 }  // namespace
 
+namespace {
+
+template <class T>
+void launch_fwd(int grid, int rows, int nch, const void* gu, void* h, uint8_t* hq, float* h_scale, uint8_t* guq,
+                float* gu_scale, hipStream_t s)
+{
+    const int stride = grid * kThreads;
+    const bool nt = (long)rows * nch * 8 * ((h ? 3 : 2) * (long)sizeof(T) + (hq ? 1 : 0) + (guq ? 2 : 0)) > kStream;
+    auto* kernel = nt ? swiglu_kernel<T, true> : swiglu_kernel<T, false>;
+    TimedLaunch tl(MOE_KID_SWIGLU, s);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, s, static_cast<const T*>(gu), rows, nch, stride / nch,
+                       stride % nch, static_cast<T*>(h), hq, h_scale, guq, gu_scale);
+}
+
+template <class T>
+void launch_bwd(int grid, int rows, int nch, const void* dh, const uint8_t* guq, const float* gu_scale, void* d_gu,
+                void* h, hipStream_t s)
+{
+    const int stride = grid * kThreads;
+    const bool nt = (long)rows * nch * 8 * ((h ? 4 : 3) * (long)sizeof(T) + 2) > kStream;
+    auto* kernel = nt ? swiglu_backward_kernel<T, true> : swiglu_backward_kernel<T, false>;
+    TimedLaunch tl(MOE_KID_SWIGLU_BWD, s);
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, s, static_cast<const T*>(dh), guq, gu_scale, rows, nch,
+                       stride / nch, stride % nch, static_cast<T*>(d_gu), static_cast<T*>(h));
+}
+
+}  // namespace
+
 moe_status launch_swiglu(const void* gu, int dt, int rows, int I, void* h, uint8_t* hq, float* h_scale,
                          uint8_t* guq, float* gu_scale, hipStream_t s)
 {
-    const int nch = I / 8, grid = grid_of(rows, nch), stride = grid * kThreads;
-    {
-        TimedLaunch tl(MOE_KID_SWIGLU, s);
-        if (dt == MOE_BF16)
-            hipLaunchKernelGGL(swiglu_kernel<bf16_t>, dim3(grid), dim3(kThreads), 0, s,
-                               static_cast<const bf16_t*>(gu), rows, nch, stride / nch, stride % nch,
-                               static_cast<bf16_t*>(h), hq, h_scale, guq, gu_scale);
-        else
-            hipLaunchKernelGGL(swiglu_kernel<float>, dim3(grid), dim3(kThreads), 0, s,
-                               static_cast<const float*>(gu), rows, nch, stride / nch, stride % nch,
-                               static_cast<float*>(h), hq, h_scale, guq, gu_scale);
-    }
+    auto* f = dt == MOE_BF16 ? launch_fwd<bf16_t> : launch_fwd<float>;
+    f(grid_of(rows, I / 8), rows, I / 8, gu, h, hq, h_scale, guq, gu_scale, s);
     return launch_status("swiglu_kernel");
 }
 
 moe_status launch_swiglu_backward(const void* dh, int dt, const uint8_t* guq, const float* gu_scale, int rows,
                                   int I, void* d_gu, void* h, hipStream_t s)
 {
-    const int nch = I / 8, grid = grid_of(rows, nch), stride = grid * kThreads;
-    {
-        TimedLaunch tl(MOE_KID_SWIGLU_BWD, s);
-        if (dt == MOE_BF16)
-            hipLaunchKernelGGL(swiglu_backward_kernel<bf16_t>, dim3(grid), dim3(kThreads), 0, s,
-                               static_cast<const bf16_t*>(dh), guq, gu_scale, rows, nch, stride / nch,
-                               stride % nch, static_cast<bf16_t*>(d_gu), static_cast<bf16_t*>(h));
-        else
-            hipLaunchKernelGGL(swiglu_backward_kernel<float>, dim3(grid), dim3(kThreads), 0, s,
-                               static_cast<const float*>(dh), guq, gu_scale, rows, nch, stride / nch,
-                               stride % nch, static_cast<float*>(d_gu), static_cast<float*>(h));
-    }
+    auto* f = dt == MOE_BF16 ? launch_bwd<bf16_t> : launch_bwd<float>;
+    f(grid_of(rows, I / 8), rows, I / 8, dh, guq, gu_scale, d_gu, h, s);
     return launch_status("swiglu_backward_kernel");
 }
 
