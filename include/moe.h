@@ -352,7 +352,8 @@ moe_status moe_expert_ffn_fp8_fused(const uint8_t* xq, const float* x_scale, int
  *     y = z * rsqrt(mean(z^2) + eps) * weight
  * The norm is taken of the rounded z, the value the residual stream carries
  * on, so that moe_rmsnorm_backward, which reads it, differentiates the same
- * function.
+ * function.  Squares are summed in fp32: |z| up to about 1e17.  A row's result
+ * does not depend on T.
  *
  *  x         device [T, H] in `dt`.
  *  residual  device [T, H] in `dt` or NULL.
@@ -372,8 +373,8 @@ moe_status moe_rmsnorm(const void* x, const void* residual, const void* weight, 
 
 /*
  * moe_rmsnorm_backward -- gradients of moe_rmsnorm (through y):
- *     c = rsqrt(mean(z^2) + eps),  g = dy * weight
- *     dz = c g - z c^3 mean(g z) (+ dtotal),   dweight = sum_t dy_t z_t c_t
+ *     c = rsqrt(mean(z^2) + eps),  n = z c,  g = dy * weight
+ *     dz = c (g - n mean(g n)) (+ dtotal),   dweight = sum_t dy_t n_t
  * dz is the gradient of x and of the residual alike.
  *
  *  dy       device [T, H] in `dt`: gradient of y.

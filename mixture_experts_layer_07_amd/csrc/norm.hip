@@ -1,12 +1,22 @@
 // moe_rmsnorm and its gradients.
 //
-//     z = x (+ residual, rounded),  c = 1 / sqrt(mean(z^2) + eps),  y = z c w
-//     g = dy w,  dz = c g - z c^3 mean(g z) (+ dtotal),  dw = sum_t dy z c
+//     z = x (+ residual, rounded),  c = 1 / sqrt(mean(z^2) + eps),  n = z c,  y = n w
+//     g = dy w,  dz = c (g - n mean(g n)) (+ dtotal),  dw = sum_t dy n
 //
-// A row stays in registers between its reduction and its outputs, so every
-// array is read and written once.  A wave owns a row of up to 2048 values,
-// a workgroup a longer one; a thread holds NV chunks of 8 consecutive values
-// at chunk indices tid, tid + stride, ...
+// Bound by memory: a row stays in registers between its reduction and its
+// outputs, so every array is read and written once.  A wave or, for longer
+// rows, a workgroup owns a row; a thread holds NV chunks of 8 consecutive
+// values at chunk indices tid, tid + stride, ...
+//
+// Measured on MI355X (8192 x 7168 bf16, a copy moves 5.1-6.5 TB/s):
+//   forward with residual, y and codes  84 us, 6.3 TB/s.  Two chunks a thread:
+//     one 91 us, four 85 us; without the streaming hints 94.6 us.
+//   backward with dtotal  84 us, 5.6 TB/s (the kernel 79 us, the sum of the
+//     partial rows 5 us).  256 or 1024 partial rows instead of 512: 104 / 90 us;
+//     two chunks a thread 85 us, one 104 us; the next row's loads in flight over
+//     the reduction 85-105 us (registers), kept only where a row is a chunk a
+//     lane.
+//   one token 5 us a call, 63 x 256 fp32 backward 7 us: launches.
 #include <algorithm>
 
 #include "rowops.h"
@@ -16,7 +26,6 @@ namespace {
 
 constexpr int kMaxWaves = 16;
 constexpr int kPartials = 512;  // most partial rows of dweight (sets the workspace's size)
-constexpr int kFewRows = 512;   // up to here the forward pass gives a row one chunk a thread
 
 // Sums of N values over the row's threads: one wave, or the workgroup through
 // LDS.  `buf` alternates between two halves on consecutive calls, so one
@@ -114,13 +123,14 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const T* x, 
 // registers; its sum is one row of `part`.  The next row's loads are issued
 // before the current row's reduction where the registers hold both rows.
 template <class T, int NV, bool WAVE, bool NT>
-__global__ __launch_bounds__(WAVE ? 1024 : 512) void rmsnorm_backward_kernel(
+__global__ __launch_bounds__(!WAVE ? 512 : NV == 4 ? 256 : 1024) void rmsnorm_backward_kernel(
     const T* dy, const T* z, const T* weight, const T* dtotal, int rows, int H, float eps, T* dz,
     float* __restrict__ part)
 {
     constexpr bool kAhead = WAVE && NV == 1;
     __shared__ float s_sum[2][kMaxWaves][2];
-    __shared__ float s_dw[WAVE ? 8 : 1][WAVE ? 512 * NV : 1];
+    constexpr int kAdd = NV == 4 ? 4 : 8;  // waves whose sums are in LDS together
+    __shared__ float s_dw[WAVE ? kAdd : 1][WAVE ? 512 * NV : 1];
     int buf = 0;
     const int wave = threadIdx.x >> 6;
     const int tid = WAVE ? (threadIdx.x & 63) : threadIdx.x;
@@ -173,15 +183,16 @@ __global__ __launch_bounds__(WAVE ? 1024 : 512) void rmsnorm_backward_kernel(
             }
         row_sum<WAVE, 2>(sum, s_sum, buf);
         const float cn = rsqrtf(sum[0] * inv + eps);
-        const float m = sum[1] * inv * cn * cn * cn;
+        const float mean = sum[1] * inv * cn;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * stride;
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                v[e] = cn * (cur.g[i][e] * w[i][e]) - cur.z[i][e] * m + cur.d[i][e];
-                dw[i][e] += cur.g[i][e] * (cur.z[i][e] * cn);
+                const float n = cur.z[i][e] * cn;
+                v[e] = cn * (cur.g[i][e] * w[i][e] - n * mean) + cur.d[i][e];
+                dw[i][e] += cur.g[i][e] * n;
             }
             if (c < nch) {
                 Raw8<T> o;
@@ -192,24 +203,26 @@ __global__ __launch_bounds__(WAVE ? 1024 : 512) void rmsnorm_backward_kernel(
         if constexpr (kAhead) cur = next;
     }
     float* out = part + (size_t)blockIdx.x * H;
-    if constexpr (WAVE) {  // the waves' sums, added in order, eight waves at a time
-        float v[4] = {0.f, 0.f, 0.f, 0.f};  // a 256-thread workgroup has up to 4 columns a thread
-        for (int k0 = 0; k0 < per; k0 += 8) {
-            if (wave >= k0 && wave < k0 + 8) {
+    if constexpr (WAVE) {  // the waves' sums, added in order, kAdd waves at a time
+        float v[2 * NV];  // a 256-thread workgroup has up to 2 NV columns a thread
+#pragma unroll
+        for (int q = 0; q < 2 * NV; ++q) v[q] = 0.0f;
+        for (int k0 = 0; k0 < per; k0 += kAdd) {
+            if (wave >= k0 && wave < k0 + kAdd) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) store8_f32(&s_dw[wave - k0][8 * (tid + 64 * i)], dw[i]);
             }
             __syncthreads();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 2 * NV; ++q) {
                 const int h = threadIdx.x + q * blockDim.x;
                 if (h < H)
-                    for (int k = 0; k < min(8, per - k0); ++k) v[q] += s_dw[k][h];
+                    for (int k = 0; k < min(kAdd, per - k0); ++k) v[q] += s_dw[k][h];
             }
             __syncthreads();
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2 * NV; ++q) {
             const int h = threadIdx.x + q * blockDim.x;
             if (h < H) out[h] = v[q];
         }
@@ -255,20 +268,16 @@ struct Shape {
     int grid;
 };
 
+// The same for every T, so a row's result does not depend on how many rows
+// there are beside it.
 Shape forward_shape(int T, int H)
 {
     const int nch = H / 8;
     Shape s;
-    s.wave = nch <= 256;
-    if (s.wave) {
-        s.threads = 256;
-        s.nv = nch <= 64 ? 1 : nch <= 128 ? 2 : 4;
-        s.per = 4;
-    } else {
-        s.nv = T <= kFewRows && nch <= 1024 ? 1 : 2;
-        s.threads = (nch + 64 * s.nv - 1) / (64 * s.nv) * 64;
-        s.per = 1;
-    }
+    s.wave = nch <= 128;
+    s.nv = nch <= 64 ? 1 : 2;
+    s.threads = s.wave ? 256 : (nch + 127) / 128 * 64;
+    s.per = s.wave ? 4 : 1;
     s.grid = std::min((T + s.per - 1) / s.per, 1 << 20);
     return s;
 }
@@ -277,14 +286,14 @@ Shape backward_shape(int T, int H)
 {
     const int nch = H / 8;
     Shape s;
-    s.wave = nch <= 128;
+    s.wave = nch <= 256;
     if (s.wave) {
-        s.threads = T <= 64 ? 1024 : 256;
-        s.nv = nch <= 64 ? 1 : 2;
+        s.nv = nch <= 64 ? 1 : nch <= 128 ? 2 : 4;
+        s.threads = T <= 64 && s.nv <= 2 ? 1024 : 256;
         s.per = s.threads / 64;
     } else {
-        s.nv = 4;
-        s.threads = (nch + 255) / 256 * 64;
+        s.nv = nch <= 512 ? 2 : 4;
+        s.threads = nch <= 1024 ? 256 : 512;
         s.per = 1;
     }
     // up to four rows one after the other cost less than the second launch that sums the partial rows
@@ -330,9 +339,8 @@ moe_status launch_rmsnorm(const void* x, const void* residual, const void* weigh
         TimedLaunch tl(MOE_KID_RMSNORM, s);
         auto go = [&](auto type) {
             using V = decltype(type);
-            auto* f = !sh.wave ? (sh.nv == 1 ? launch_fwd<V, 1, false> : launch_fwd<V, 2, false>)
-                      : sh.nv == 1 ? launch_fwd<V, 1, true>
-                      : sh.nv == 2 ? launch_fwd<V, 2, true> : launch_fwd<V, 4, true>;
+            auto* f = !sh.wave ? launch_fwd<V, 2, false>
+                      : sh.nv == 1 ? launch_fwd<V, 1, true> : launch_fwd<V, 2, true>;
             f(sh, x, residual, weight, T, H, eps, total, y, yq, y_scale, s);
         };
         if (dt == MOE_BF16) go(bf16_t{});
@@ -352,8 +360,9 @@ moe_status launch_rmsnorm_backward(const void* dy, const void* z, const void* we
         TimedLaunch tl(MOE_KID_RMSNORM_BWD, s);
         auto go = [&](auto type) {
             using V = decltype(type);
-            auto* f = !sh.wave ? launch_bwd<V, 4, false>
-                      : sh.nv == 1 ? launch_bwd<V, 1, true> : launch_bwd<V, 2, true>;
+            auto* f = !sh.wave ? (sh.nv == 2 ? launch_bwd<V, 2, false> : launch_bwd<V, 4, false>)
+                      : sh.nv == 1 ? launch_bwd<V, 1, true>
+                      : sh.nv == 2 ? launch_bwd<V, 2, true> : launch_bwd<V, 4, true>;
             f(sh, dy, z, weight, dtotal, T, H, eps, dz, part, s);
         };
         if (dt == MOE_BF16) go(bf16_t{});

@@ -1,20 +1,24 @@
 // moe_route_backward: the gradient of the routing weights.
 //
 // With a kept expert's unnormalised weight w (an exponential or a sigmoid), S
-// the sum that divides the weights and d the incoming gradients,
-//     v_j - sum_i v_i w_i / S  =  (sum_i w_i (d_j - d_i) + (S - sum_i w_i) d_j) scaling / S
-// where S - sum_i w_i is what the sum holds besides the kept weights: the
-// other experts' exponentials (plain softmax), the 1e-20 (DeepSeek-V3) or
-// nothing.  Written so, nothing cancels where one weight is near 1, and one
-// renormalised weight alone has gradient exactly 0.
+// the sum that divides the weights and d the incoming gradients, a renormalised
+// weight's gradient and a plain softmax's are both
+//     scaling * slope_j w_j / S * (d_j S - sum_i w_i d_i) / S
+// where S holds the kept weights and, for plain softmax, the other experts'
+// exponentials, for DeepSeek-V3 its 1e-20; slope is 1 for exponentials and
+// 1 - sig for sigmoids.  The kept experts are computed in fp64, so that the
+// difference keeps more digits than the output where one weight is near 1.
+// The products of the difference are rounded alike (no fused multiply-add):
+// one renormalised weight alone, which is constant, has gradient exactly 0.
 //
-// Latency-bound: it writes T*E floats and reads little.  A wave owns eight
-// tokens, eight lanes each: they compute the kept experts' gradients in fp64 (k
-// exponentials a token) and put them into a tile of the output in LDS, which is
-// then written as one contiguous run.  Plain softmax, where every logit has a
-// gradient, first reads the tile's logits as one run and takes each row's
-// statistics; the rows' walks start 8 columns apart so that the eight rows do
-// not meet in the same LDS banks.
+// Latency-bound while small, then bound by the writes (T*E floats).  A wave
+// owns eight tokens, eight lanes each: they compute the kept experts' gradients
+// (an exponential and three divisions each; sums over a token's lanes by lane
+// permutations) and put them into a tile of the output in LDS, which then goes
+// out in whole rows.  Plain softmax, where every logit has a gradient, keeps
+// the tile's logits there first and walks each row with its eight lanes.  The
+// tile's rows are 8 floats longer than E so that the eight rows' walks meet
+// different banks at E = 256.  A row's result does not depend on its place.
 #include <algorithm>
 
 #include "rowops.h"
@@ -26,159 +30,173 @@ constexpr int kTok = 8;       // tokens a wave
 constexpr int kThreads = 64;  // a workgroup is one wave: its barriers cost nothing
 constexpr int kMaxGrid = 1 << 20;
 
-template <class V>
-__device__ __forceinline__ V sum8(V v)
+// The value of the lane that DPP control `ctrl` names.
+template <int ctrl>
+__device__ __forceinline__ double dpp_f64(double v)
 {
-    v += __shfl_xor(v, 1, 64);
-    v += __shfl_xor(v, 2, 64);
-    v += __shfl_xor(v, 4, 64);
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, ctrl, 0xf, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), ctrl, 0xf, 0xf, false);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Sums and maxima over aligned groups of 8 lanes, in every lane of them.
+__device__ __forceinline__ double sum8(double v)
+{
+    v += dpp_f64<0xb1>(v);   // quad_perm [1,0,3,2]
+    v += dpp_f64<0x4e>(v);   // quad_perm [2,3,0,1]
+    v += dpp_f64<0x141>(v);  // row_half_mirror
     return v;
 }
 
-template <class V>
-__device__ __forceinline__ V max8(V v)
+__device__ __forceinline__ float sum8(float v)
 {
-    v = fmax(v, __shfl_xor(v, 1, 64));
-    v = fmax(v, __shfl_xor(v, 2, 64));
-    return fmax(v, __shfl_xor(v, 4, 64));
+    v += dpp_f32<0xb1>(v);
+    v += dpp_f32<0x4e>(v);
+    v += dpp_f32<0x141>(v);
+    return v;
 }
 
-// Calls f with the columns that lane j takes of its token's row: 8 q + j for q
-// from tl on, around the end.
-template <class F>
-__device__ __forceinline__ void walk(int E, int tl, int j, F f)
+__device__ __forceinline__ float max8(float v)
 {
-    const int n = (E + 7) >> 3;
-    int q = tl % n;
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-        const int i = 8 * q + j;
-        if (i < E) f(i);
-        q = q + 1 == n ? 0 : q + 1;
-    }
+    v = fmaxf(v, dpp_f32<0xb1>(v));
+    v = fmaxf(v, dpp_f32<0x4e>(v));
+    return fmaxf(v, dpp_f32<0x141>(v));
 }
 
+// Calls f(tile index, output index) with the lane's elements of nt rows of E.
+// W: floats at a time.
+template <int W, class F>
+__device__ __forceinline__ void rows_of(int nt, int E, int pitch, F f)
+{
+#pragma unroll
+    for (int r = 0; r < kTok; ++r)
+        if (r < nt)
+            for (int c = (int)threadIdx.x * W; c < E; c += kThreads * W) f(r * pitch + c, r * E + c);
+}
+
+// WHOLE: plain softmax.  W: 4 where E and logits allow 16-byte accesses to the
+// rows, else 1.
+template <bool WHOLE, int W>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(const float* __restrict__ logits,
-                                                             const int32_t* __restrict__ ids,
-                                                             const float* __restrict__ d_scales, int T, int E,
-                                                             int method, int k, float scaling, bool whole,
-                                                             bool aligned, float* __restrict__ d_logits)
+                                                                  const int32_t* __restrict__ ids,
+                                                                  const float* __restrict__ d_scales, int T,
+                                                                  int E, int method, int k, float scaling,
+                                                                  float* __restrict__ d_logits)
 {
-    __shared__ __align__(16) float s_out[kTok * MOE_MAX_EXPERTS];
-    const int lane = threadIdx.x & 63;
-    const int tl = threadIdx.x >> 3, j = threadIdx.x & 7;
+#pragma clang fp contract(off)
+    typedef float vec_t __attribute__((ext_vector_type(W)));
+    __shared__ __align__(16) float s_out[kTok * (MOE_MAX_EXPERTS + 8)];
+    const int lane = threadIdx.x;
+    const int tl = lane >> 3, j = lane & 7, first_lane = lane & ~7;
+    const int pitch = E + 8;
+    float* row = s_out + tl * pitch;
     const bool sigm = method == MOE_ROUTE_DEEPSEEKV3 || method == MOE_ROUTE_MINIMAX2 ||
                       method == MOE_ROUTE_SIGMOID_RENORM || method == MOE_ROUTE_LLAMA4;
     for (long t0 = (long)blockIdx.x * kTok; t0 < T; t0 += (long)gridDim.x * kTok) {
         const int nt = (int)min((long)kTok, T - t0);
         const long t = t0 + tl;
         int e = -1;
-        double d = 0.0, l = 0.0;
+        double d = 0.0;
+        float l = -INFINITY;
         if (tl < nt && j < k) {
             e = ids[t * k + j];
             d = d_scales[t * k + j];
         }
-        float* row = s_out + tl * E;
-        // the tile: zeros, or its logits (t0 * E is a multiple of 4, so a run starts on a 16-byte boundary)
-        const int n = nt * E;
+        // the tile: the rows' logits, or zeros
         const float* in = logits + t0 * E;
-        if (!whole || aligned) {
-#pragma unroll 4
-            for (int i = threadIdx.x; i < (n >> 2); i += kThreads)
-                reinterpret_cast<float4*>(s_out)[i] =
-                    whole ? reinterpret_cast<const float4*>(in)[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int i = (n & ~3) + threadIdx.x; i < n; i += kThreads) s_out[i] = whole ? in[i] : 0.0f;
-        } else {
-            for (int i = threadIdx.x; i < n; i += kThreads) s_out[i] = in[i];
-        }
+        rows_of<W>(nt, E, pitch, [&](int s, int g) {
+            *reinterpret_cast<vec_t*>(s_out + s) = WHOLE ? *reinterpret_cast<const vec_t*>(in + g) : vec_t(0.0f);
+        });
         if ((unsigned)e >= (unsigned)E) {  // a dropped pair
             e = -1;
             d = 0.0;
         }
-        if (!whole && e >= 0) l = logits[t * E + e];
-        double m = 0.0, rest = 0.0;  // maximum, and the sum of what is not kept
-        if (whole) {
-            // every expert once: the first of several pairs takes the others' gradients
-            double sum = 0.0;
-            bool first = true;
+        if (!WHOLE && e >= 0) l = logits[t * E + e];
+        // does a token list an expert twice?  (moe_route's ids do not)
+        bool again = false;
 #pragma unroll
-            for (int i = 0; i < MOE_MAX_TOPK; ++i) {
-                const int ei = __shfl(e, (lane & ~7) | i, 64);
-                const double di = __shfl(d, (lane & ~7) | i, 64);
-                if (ei == e) {
-                    sum += di;
-                    first = first && i >= j;
+        for (int i = 0; i < MOE_MAX_TOPK; ++i) again |= i != j && e >= 0 && __shfl(e, first_lane | i, 64) == e;
+        const bool twice = __any(again);
+        __syncthreads();
+        double rest = 0.0;  // what S holds besides the kept weights
+        float top = 0.0f;   // maximum logit
+        if constexpr (WHOLE) {
+            if (twice) {  // every expert once: the first of its pairs takes the others' gradients
+                double sum = 0.0;
+                bool first = true;
+                for (int i = 0; i < MOE_MAX_TOPK; ++i) {
+                    const int ei = __shfl(e, first_lane | i, 64);
+                    const double di = __shfl(d, first_lane | i, 64);
+                    if (ei == e) {
+                        sum += di;
+                        first = first && i >= j;
+                    }
                 }
+                d = first ? sum : 0.0;
+                e = first ? e : -1;
             }
-            d = first ? sum : 0.0;
-            e = first ? e : -1;
-            __syncthreads();
             if (e >= 0) l = row[e];
-            float mx = -INFINITY;
-            if (tl < nt) walk(E, tl, j, [&](int i) { mx = fmaxf(mx, row[i]); });
-            mx = max8(mx);
-            m = mx;
+            top = -INFINITY;
+            if (tl < nt) {
+#pragma unroll 8
+                for (int i = j; i < E; i += 8) top = fmaxf(top, row[i]);
+            }
+            top = max8(top);
             __syncthreads();
             if (e >= 0) row[e] = -INFINITY;  // the kept ones are added in fp64 below
             __syncthreads();
             float z = 0.0f;
-            if (tl < nt)
-                walk(E, tl, j, [&](int i) {
-                    const float p = mx == -INFINITY ? 0.0f : expf(row[i] - mx);
+            if (tl < nt) {
+#pragma unroll 8
+                for (int i = j; i < E; i += 8) {
+                    const float p = top == -INFINITY ? 0.0f : expf(row[i] - top);
                     row[i] = p;
                     z += p;
-                });
-            rest = sum8((double)z);
+                }
+            }
+            rest = sum8(z);
         } else if (!sigm) {
-            m = max8(e >= 0 ? l : (double)-INFINITY);
+            top = max8(l);
         }
-        double w = 0.0, slope = 1.0;  // the weight before division, and its own slope over itself
+        double w = 0.0, slope = 1.0;
         if (e >= 0) {
             if (sigm) {
-                const double x = exp(-fabs(l));
-                w = l >= 0.0 ? 1.0 / (1.0 + x) : x / (1.0 + x);
-                slope = l >= 0.0 ? x / (1.0 + x) : 1.0 / (1.0 + x);
+                const double x = exp(-fabs((double)l)), y = 1.0 / (1.0 + x);
+                w = l >= 0.0f ? y : x * y;
+                slope = l >= 0.0f ? x * y : y;
             } else {
-                w = m == -INFINITY ? 0.0 : exp(l - m);
+                w = top == -INFINITY ? 0.0 : exp((double)l - top);
             }
         }
         if (method == MOE_ROUTE_DEEPSEEKV3) rest = 1e-20;
-        double v = 0.0, mean = 0.0;
-        const double S = sum8(w) + rest;
-        if (method == MOE_ROUTE_LLAMA4) {
-            v = d * w * slope;
-        } else {
-            double a = rest * d;
-#pragma unroll
-            for (int i = 0; i < MOE_MAX_TOPK; ++i) {
-                const double wi = __shfl(w, (lane & ~7) | i, 64), di = __shfl(d, (lane & ~7) | i, 64);
-                a += wi * (d - di);
-                mean += wi * di;
-            }
-            v = S > 0.0 ? w / S * slope * (a / S) : 0.0;
-            mean = S > 0.0 ? mean / S / S : 0.0;
-        }
+        const double S = sum8(w) + rest, wd = sum8(w * d);
+        double v;
+        if (method == MOE_ROUTE_LLAMA4) v = w * slope * d;
+        else v = S > 0.0 ? w / S * slope * ((S * d - wd) / S) : 0.0;
         v *= scaling;
-        // an expert listed twice gets the sum, written by both lanes
-        double both = 0.0;
-#pragma unroll
-        for (int i = 0; i < MOE_MAX_TOPK; ++i) {
-            const int ei = __shfl(e, (lane & ~7) | i, 64);
-            const double vi = __shfl(v, (lane & ~7) | i, 64);
-            if (ei == e) both += vi;
+        if constexpr (WHOLE) {
+            const float f = S > 0.0 ? (float)(wd / S / S * -scaling) : 0.0f;
+            if (tl < nt) {
+#pragma unroll 8
+                for (int i = j; i < E; i += 8) row[i] *= f;
+            }
+            __syncthreads();
+        } else if (twice) {  // both lanes write the sum
+            double both = 0.0;
+            for (int i = 0; i < MOE_MAX_TOPK; ++i) {
+                const int ei = __shfl(e, first_lane | i, 64);
+                const double vi = __shfl(v, first_lane | i, 64);
+                if (ei == e) both += vi;
+            }
+            v = both;
         }
-        __syncthreads();
-        if (whole && tl < nt) {
-            const float f = (float)(-mean * scaling);
-            walk(E, tl, j, [&](int i) { row[i] *= f; });
-        }
-        if (whole) __syncthreads();
-        if (e >= 0) row[e] = (float)both;
+        if (e >= 0) row[e] = (float)v;
         __syncthreads();
         float* out = d_logits + t0 * E;
-        for (int i = threadIdx.x; i < (n >> 2); i += kThreads)
-            reinterpret_cast<float4*>(out)[i] = reinterpret_cast<const float4*>(s_out)[i];
-        for (int i = (n & ~3) + threadIdx.x; i < n; i += kThreads) out[i] = s_out[i];
+        rows_of<W>(nt, E, pitch, [&](int s, int g) {
+            *reinterpret_cast<vec_t*>(out + g) = *reinterpret_cast<const vec_t*>(s_out + s);
+        });
         __syncthreads();
     }
 }
@@ -190,11 +208,14 @@ moe_status launch_route_backward(const float* logits, const int32_t* ids, const 
                                  hipStream_t s)
 {
     const bool whole = method == MOE_ROUTE_DEFAULT && !(flags & MOE_ROUTE_FLAG_RENORMALIZE);
+    const bool wide = E % 4 == 0 && !(whole && (reinterpret_cast<uintptr_t>(logits) & 15));
+    auto* kernel = whole ? (wide ? route_backward_kernel<true, 4> : route_backward_kernel<true, 1>)
+                         : (wide ? route_backward_kernel<false, 4> : route_backward_kernel<false, 1>);
     const int grid = (int)std::min(((long)T + kTok - 1) / kTok, (long)kMaxGrid);
     {
         TimedLaunch tl(MOE_KID_ROUTE_BWD, s);
-        hipLaunchKernelGGL(route_backward_kernel, dim3(grid), dim3(kThreads), 0, s, logits, ids, d_scales, T, E, method,
-                           k, scaling, whole, (reinterpret_cast<uintptr_t>(logits) & 15) == 0, d_logits);
+        hipLaunchKernelGGL(kernel, dim3(grid), dim3(kThreads), 0, s, logits, ids, d_scales, T, E, method, k, scaling,
+                           d_logits);
     }
     return launch_status("route_backward_kernel");
 }

@@ -177,7 +177,9 @@ def test_rmsnorm_special_rows(dt):
 
 
 def dweight_depth(T, H):
-    """Additions in the longest chain of dweight: a partial sum's rows, its waves, 16 partials, 32 runs."""
+    """Additions in the longest chain of dweight: a partial sum's rows (4 in a row at least before the
+    rows are spread over up to 512 sums of 4 waves), its waves (4, or 16 that then are all), the 16
+    partial sums of a run, 32 runs."""
     per = 4 if H <= 2048 else 1
     return -(-T // (512 * per)) + 4 + 16 + 32
 
@@ -224,6 +226,17 @@ def test_rmsnorm_backward_against_differences():
         # sums of T*H terms of order 1, each off by some 2^-18
         assert abs(float((dz.cpu().to(F64) * v).sum()) - a) < 1e-2
         assert abs(float((dw.cpu().to(F64) * u).sum()) - b) < 1e-2
+
+
+def test_rmsnorm_backward_tiny_eps():
+    """A zero row under a tiny eps: c is large, its third power would overflow."""
+    T, H = 5, 256
+    z, w, dy = rnd(T, H), torch.ones(H), rnd(T, H, seed=2)
+    z[2] = 0
+    dz, dw = moe.rmsnorm_backward(dy.to(DEV), z.to(DEV), w.to(DEV), 1e-30)
+    want, wantw, size, sizew = ref.rmsnorm_backward(dy, z, w, float(np.float32(1e-30)))
+    within(dz, want, want.abs() * half_step(FP) + size * (3 * NORM + 8 * EPS32) * 1.01, "dz")
+    within(dw, wantw, sizew * ((dweight_depth(T, H) + 2) * EPS32 + NORM), "dweight")
 
 
 def test_rmsnorm_backward_of_no_rows():

@@ -1,0 +1,157 @@
+"""The row operators at sizes where counters and offsets could end: more rows than
+the largest grid has workgroups, arrays past 2^31 values and 2^32 bytes; and two
+threads that call them at once.
+
+Rows are independent, so rows of a large call are compared bit for bit with a
+call on those rows alone (the other tests hold that one to the 64-bit forms), at
+the start, across the borders and at the end."""
+import threading
+
+import pytest
+import torch
+
+import mixture_experts_layer_07_amd as moe
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda"
+BF, FP = torch.bfloat16, torch.float32
+
+
+def rnd(*shape, seed=0, dt=BF):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    out = torch.empty(shape, dtype=dt, device=DEV)
+    step = max(1, (1 << 28) // max(1, shape[-1]))
+    for a in range(0, shape[0], step):
+        out[a:a + step] = torch.randn((min(step, shape[0] - a),) + shape[1:], generator=g, device=DEV)
+    return out
+
+
+def spans(T, *borders):
+    """Row ranges at the start, around each border and at the end."""
+    at = [(0, 5), (T - 5, T)] + [(max(0, b - 3), min(T, b + 3)) for b in borders if b < T]
+    return [(a, b) for a, b in at if a < b]
+
+
+def same(a, b, what):
+    torch.cuda.synchronize()
+    assert a.dtype == b.dtype and a.shape == b.shape and torch.equal(a.contiguous().view(torch.uint8),
+                                                                     b.contiguous().view(torch.uint8)), what
+
+
+NORMS = [(4 * (1 << 20) + 7, 8, 4 << 20), ((1 << 20) + 3, 1032, 1 << 20), (300_003, 7168, (1 << 31) // 7168)]
+
+
+@pytest.mark.parametrize("T,H,border", NORMS)
+def test_rmsnorm(T, H, border):
+    x, r, w = rnd(T, H), rnd(T, H, seed=1), rnd(1, H, seed=2)[0]
+    q = H % 128 == 0
+    got = moe.rmsnorm(x, w, residual=r, quantize=q)
+    for a, b in spans(T, border, border // 2):
+        part = moe.rmsnorm(x[a:b].clone(), w, residual=r[a:b].clone(), quantize=q)
+        for m, n, what in zip(got, part, ("y", "total", "codes", "scales")):
+            if m is not None:
+                same(m[a:b], n, f"{what} of rows {a} to {b}")
+
+
+@pytest.mark.parametrize("T,H,border", NORMS)
+def test_rmsnorm_backward(T, H, border):
+    z, dy, w = rnd(T, H), rnd(T, H, seed=1), rnd(1, H, seed=2)[0]
+    dz, dw = moe.rmsnorm_backward(dy, z, w)
+    want, size = torch.zeros(H, dtype=torch.float64, device=DEV), torch.zeros(H, dtype=torch.float64, device=DEV)
+    step = (1 << 28) // H
+    for a in range(0, T, step):
+        zz, gg = z[a:a + step].double(), dy[a:a + step].double()
+        t = zz * gg * (zz.square().mean(1, keepdim=True) + 1e-6).rsqrt()
+        want += t.sum(0)
+        size += t.abs().sum(0)
+    # chains of the rows of one partial sum and the adding of the sums (up to 100), the norm's own 48
+    chain = -(-T // 512) + 100 + 48
+    assert bool(((dw.double() - want).abs() <= size * chain * 2.0 ** -24).all())
+    for a, b in spans(T, border, border // 2):
+        same(dz[a:b], moe.rmsnorm_backward(dy[a:b].clone(), z[a:b].clone(), w)[0], f"rows {a} to {b}")
+
+
+@pytest.mark.parametrize("T,H,k,sh", [((1 << 20) + 9, 16, 2, 1), (40_003, 7168, 7, 1)])
+def test_rows_in_expert_order(T, H, k, sh):
+    P = T * k
+    g = torch.Generator(device=DEV).manual_seed(3)
+    up = torch.randperm(P, generator=g, device=DEV).int()
+    x = rnd(T, H)
+    rows = moe.dispatch(x, up, k, sh)
+    sample = torch.cat([torch.arange(a, b, device=DEV) for a, b in spans(T, 1 << 20)])
+    sample = torch.cat([sample, torch.randint(0, T, (500,), generator=g, device=DEV)])
+    for j in range(k):
+        same(rows[up.view(T, k)[sample, j].long()], x[sample], f"pair {j}")
+    same(rows[P + sample], x[sample], "shared rows")
+    del rows
+    d = rnd(P + sh * T, H, seed=4)
+    dx = moe.dispatch_backward(d, up, k, sh)
+    dy, sc = rnd(T, H, seed=5), rnd(T, k, seed=6, dt=FP)
+    d_fc2, ds = moe.finalize_backward(dy, d, up, sc, sh)
+    # the sampled tokens alone, with their rows brought together
+    n = sample.numel()
+    here = torch.arange(n * k, device=DEV).int()
+    part = torch.cat([d[up.view(T, k)[sample].reshape(-1).long()], d[P + sample]])
+    same(dx[sample], moe.dispatch_backward(part, here, k, sh), "dx")
+    p_fc2, p_ds = moe.finalize_backward(dy[sample].contiguous(), part, here, sc[sample].contiguous(), sh)
+    same(ds[sample], p_ds, "d_scales")
+    same(d_fc2[up.view(T, k)[sample].reshape(-1).long()], p_fc2[:n * k], "d_fc2")
+    same(d_fc2[P + sample], p_fc2[n * k:], "d_fc2 of shared rows")
+
+
+@pytest.mark.parametrize("method", [0, 2])
+@pytest.mark.parametrize("T,E,border", [(8 * (1 << 20) + 5, 4, 8 << 20), ((1 << 23) + 77, 256, 1 << 23)])
+def test_route_backward(T, E, border, method):
+    l, ds = rnd(T, E, dt=FP), rnd(T, 2, seed=1, dt=FP)
+    ids = torch.stack([torch.arange(T, device=DEV) % E, (torch.arange(T, device=DEV) + 1) % E], 1).int()
+    got = moe.route_backward(l, ids, ds, method)
+    for a, b in spans(T, border, border // 2):
+        same(got[a:b], moe.route_backward(l[a:b].clone(), ids[a:b].clone(), ds[a:b].clone(), method), f"rows {a} to {b}")
+
+
+@pytest.mark.parametrize("rows,I", [((1 << 20) + 5, 1024), (70_001, 16384)])
+def test_swiglu(rows, I):
+    gu = rnd(rows, 2 * I)
+    got = moe.swiglu(gu, quantize=True, checkpoint=True, want_h=True)
+    dh = got[0]
+    back = moe.swiglu_backward(dh, got[3], got[4], want_h=True)
+    for a, b in spans(rows, (1 << 30) // I, (1 << 31) // I):
+        part = moe.swiglu(gu[a:b].clone(), quantize=True, checkpoint=True, want_h=True)
+        for m, n, what in zip(got, part, ("h", "codes", "scales", "checkpoint", "its scales")):
+            same(m[a:b], n, f"{what} of rows {a} to {b}")
+        for m, n, what in zip(back, moe.swiglu_backward(part[0], part[3], part[4], want_h=True), ("d_gu", "h again")):
+            same(m[a:b], n, f"{what} of rows {a} to {b}")
+
+
+def test_two_threads():
+    """Two threads on streams of their own: every result is the one the call gives alone."""
+    T, H = 257, 1024
+    sets = [(rnd(T, H, seed=s), rnd(T, H, seed=s + 1), rnd(1, H, seed=s + 2)[0]) for s in (0, 10)]
+    want = [moe.rmsnorm(x, w, residual=r, quantize=True) + moe.rmsnorm_backward(r, x, w) for x, r, w in sets]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        x, r, w = sets[i]
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for n in range(50):
+                got = moe.rmsnorm(x, w, residual=r, quantize=True) + moe.rmsnorm_backward(r, x, w)
+                s.synchronize()
+                for a, b in zip(got, want[i]):
+                    if not torch.equal(a.view(torch.uint8), b.view(torch.uint8)):
+                        bad.append((i, n))
+                try:
+                    moe.rmsnorm(x, w, eps=0.0)
+                    bad.append((i, "no error"))
+                except moe.MoeError as e:  # the reason is the calling thread's own
+                    if "eps" not in str(e):
+                        bad.append((i, str(e)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad[:5]

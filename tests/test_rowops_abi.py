@@ -210,3 +210,45 @@ def test_binding_refuses_host_tensors():
     for call in calls:
         with pytest.raises(ValueError, match="must be a GPU tensor"):
             call()
+
+
+# ----------------------------------------------------- the binding's native half
+def test_call_checks_its_arguments(L):
+    """Wrong counts, numbers that do not fit and buffers that are none are refused before the
+    device is touched."""
+    a = (None, 1, None, None, 1, 1, 8, 0, None, 0)
+    for args, error in ((a[:-1], TypeError), (a + (0,), TypeError), ((3,) + a[1:], TypeError),
+                        (a[:4] + (2 ** 31,) + a[5:], OverflowError), (a[:4] + (1.5,) + a[5:], TypeError),
+                        ((torch.zeros(8),) + a[1:], ValueError)):
+        with pytest.raises(error):
+            binding._call("moe_finalize", "cuda:0", *args)
+    with pytest.raises(AttributeError, match="no entry point moe_nothing"):
+        binding._call("moe_nothing", "cuda:0")
+    with pytest.raises(TypeError):
+        binding._marshal.call("moe_finalize", "cuda:0", *a)  # a torch.device
+
+
+def test_call_covers_every_kernel_entry():
+    """Each entry point that launches is known to the native half (it asks for its arguments)."""
+    import re
+    text = open(__file__.replace("tests/test_rowops_abi.py", "include/moe.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    launching = re.findall(r"moe_status (moe_\w+)\([^;]*void\* stream\);", text)
+    assert len(launching) >= 17
+    for fn in launching:
+        with pytest.raises(TypeError, match=fn):
+            binding._call(fn, "cuda:0")
+
+
+def test_check_accepts_and_refuses():
+    x = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="x must be a GPU tensor"):
+        binding._dev(x, "x", torch.float32, (4, 8))
+    with pytest.raises(ValueError, match="x must be a GPU tensor"):
+        binding._dev(x, "x", shape=(4, 8))
+    with pytest.raises(AttributeError):
+        binding._dev(None, "x", torch.float32)
+    for call in (lambda: binding._dev(), lambda: binding._dev(x), lambda: binding._dev(x, "x", type=3),
+                 lambda: binding._dev(x, "x", None, None, None)):
+        with pytest.raises(TypeError):
+            call()
