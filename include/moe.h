@@ -408,7 +408,7 @@ size_t moe_rmsnorm_backward_workspace_size(int T, int H);
  *  x          device [T, H] in `dt`, which may also be MOE_FP8_E4M3: codes,
  *             with x_scale [T, H/128], as moe_quantize_fp8 or moe_rmsnorm
  *             write them.
- *  H          a multiple of 8 (fp8: of 128).
+ *  H          a multiple of 8 (fp8: of 128), at most 2^28.
  *  unpermute  device int32 [T*k] from moe_permute.  A pair whose entry lies
  *             outside [0, T*k) is dropped: no row is written for it.
  *  rows       device [T*k + n_shared*T, H] in `dt` out.  Rows that no pair
@@ -428,7 +428,7 @@ moe_status moe_dispatch(const void* x, const float* x_scale, int dt, int T, int 
  *
  *  d_rows  device [T*k + n_shared*T, H] in `dt`.
  *  dx      device [T, H] in `dxt` (MOE_F32 or MOE_BF16) out.
- *  H       a multiple of 8.
+ *  H       as for moe_dispatch.
  */
 moe_status moe_dispatch_backward(const void* d_rows, int dt, const int32_t* unpermute, int T, int k,
                                  int H, int n_shared, void* dx, int dxt, void* stream);
@@ -444,7 +444,7 @@ moe_status moe_dispatch_backward(const void* d_rows, int dt, const int32_t* unpe
  *            [0, T*k)) gets d_scales 0, and no row is written for it.
  *  d_fc2     device [T*k + n_shared*T, H] in `dt` out; may be fc2_out itself.
  *  d_scales  device fp32 [T, k] out: what moe_route_backward takes.
- *  H         a multiple of 8.
+ *  H         a multiple of 8, at most 2^28.
  */
 moe_status moe_finalize_backward(const void* dy, int dyt, const void* fc2_out, int dt,
                                  const int32_t* unpermute, const float* scales, int T, int k, int H,

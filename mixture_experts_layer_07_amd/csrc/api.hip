@@ -494,6 +494,7 @@ static moe_status check_places(int T, int k, int H, int n_shared)
     if (n_shared < 0 || n_shared > 64) return set_error(MOE_ERR_INVALID_ARG, "n_shared must be in [0, 64]");
     if (H < 1) return set_error(MOE_ERR_INVALID_ARG, "H must be positive");
     if (H % 8) return set_error(MOE_ERR_UNSUPPORTED, "H must be a multiple of 8 (got %d)", H);
+    if (H > (1 << 28)) return set_error(MOE_ERR_UNSUPPORTED, "H = %d exceeds 2^28", H);
     if ((long long)T * k + (long long)n_shared * T > (1ll << 30))
         return set_error(MOE_ERR_UNSUPPORTED, "too many rows");
     return MOE_OK;

@@ -134,7 +134,7 @@ def test_dispatch_validation(L):
     assert f(dt=FP8) == INVALID and f(dt=FP8, xs=P) == INVALID and f(xs=P, rs=P) == INVALID
     assert f(x=None) == INVALID and f(up=None) == INVALID and f(rows=None) == INVALID
     assert f(x=ODD) == INVALID and f(rows=ODD) == INVALID
-    assert f(T=1 << 29, k=4) == UNSUPPORTED
+    assert f(T=1 << 29, k=4) == UNSUPPORTED and f(H=(1 << 28) + 8) == UNSUPPORTED
     assert f(T=0, x=None, up=None, rows=None) == OK
 
     def g(d=P, dt=BF16, up=P, T=4, k=2, H=256, sh=0, dx=P, dxt=BF16):
