@@ -5,6 +5,12 @@
 // the whole workgroup), and each thread moves 16-byte words of the row: a
 // token's row is read once and written to all its places, or its places'
 // rows are read and summed.  No atomics: every row belongs to one token.
+//
+// Bound by memory.  Measured on MI355X, 8192 tokens x 7168 bf16, k = 8, one shared
+// expert, skewed routing (1.17 GB a copy): dispatch and its gradient in turn 440
+// us (5.3 TB/s; each alone 187 and 178 us), the gradients of finalize 384 us (2.1
+// GB, 5.5 TB/s; 338 us with rows in token order).  Decode batch of 512 tokens'
+// codes 7.1 us.
 #include <algorithm>
 
 #include "rowops.h"
@@ -14,52 +20,41 @@ namespace {
 
 constexpr int kMaxGrid = 1 << 20;
 
-// A thread for each 16-byte word (or 8 values) of a row, up to 1024: the whole
-// row moves at once, which the memory likes better than four steps of 4 KiB
-// (DeepSeek-V3-shaped training batch, 256 -> 1024 threads at most: gradients of
-// the weighted sum 413 -> 391 us, dispatch and its gradient 456 -> 446 us).
-int threads_for(int n) { return std::min(1024, (n + 63) / 64 * 64); }
+// A thread for each 16-byte word of a row, up to 512 or (wide) 1024.  With many
+// rows a token the whole row at once is what the memory likes best; with few, a
+// workgroup of 1024 threads waits too long for too little.  512 / 1024 threads:
+//   dispatch and gradient, 4096 x 7168 bf16  k = 1 47 / 64 us, k = 2 65 / 74 us,
+//     k = 4 110 / 105 us; 8192 tokens, k = 8 and a shared expert 463 / 446 us
+//   finalize_backward, 4096 x 7168 bf16  k = 1 34 / 52 us, k = 2 53 / 63 us, k = 4
+//     96.5 / 97.0 us, k = 6 142 / 140 us; 512 tokens, k = 8 25.8 / 27.7 us; 64 x
+//     7168 fp32, k = 8 12.9 / 10.8 us
+int threads_for(int n, bool wide) { return std::min(wide ? 1024 : 512, (n + 63) / 64 * 64); }
 
-// 16 bytes at byte `off` of a row at a wave-uniform address.  Streamed rows are
-// written once by one workgroup and fill the caches with nothing but
-// themselves.  THROUGH: past this XCD's L2 as well (a buffer store with the
-// device scope and non-temporal bits), so that no dirty lines are left for the
-// next kernel to write back.  Dispatch and gradient of the DeepSeek-V3-shaped
-// training batch: plain 442 us, non-temporal 439, THROUGH 427; its fp8 rows
-// alone 107, 88, 80; the 33 MB of a decode batch 7.9, 7.1, 7.8 us.
-template <bool THROUGH>
-__device__ __forceinline__ void store_row16(u32x4_t v, char* row, unsigned row_bytes, unsigned off)
-{
-    if constexpr (THROUGH) {
-        constexpr int kNt = 2, kSc1 = 16;
-        const auto r = __builtin_amdgcn_make_buffer_rsrc(row, 0, (int)row_bytes, 0x00027000);
-        __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, kNt | kSc1);
-    } else {
-        __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(row + off));
-    }
-}
-
-// Rows of `bytes` bytes (a multiple of 16); with scales, nsc floats a row.
-template <bool THROUGH>
-__global__ __launch_bounds__(1024) void dispatch_kernel(const char* __restrict__ x,
+// Rows of nch 16-byte words; with scales, nsc floats a row.  A row is written
+// once, by one workgroup, and fills the caches with nothing but itself: the
+// stores carry the non-temporal hint at every size (plain / hinted: 33 MB of a
+// decode batch's codes 7.9 / 7.1 us, with a reader behind them equal; 530 MB of
+// codes 107 / 88 us).
+__global__ __launch_bounds__(1024) void dispatch_kernel(const u32x4_t* __restrict__ x,
                                                         const float* __restrict__ x_scale, int T, int k,
-                                                        int n_shared, unsigned bytes, int nsc,
+                                                        int n_shared, int nch, int nsc,
                                                         const int32_t* __restrict__ unpermute,
-                                                        char* __restrict__ rows, float* __restrict__ rows_scale)
+                                                        u32x4_t* __restrict__ rows,
+                                                        float* __restrict__ rows_scale)
 {
     const int P = T * k;
     for (int t = blockIdx.x; t < T; t += gridDim.x) {
         int at[MOE_MAX_TOPK];
 #pragma unroll
         for (int j = 0; j < MOE_MAX_TOPK; ++j) at[j] = j < k ? unpermute[(size_t)t * k + j] : -1;
-        for (unsigned c = threadIdx.x * 16; c < bytes; c += blockDim.x * 16) {
-            const u32x4_t v = *reinterpret_cast<const u32x4_t*>(x + (size_t)t * bytes + c);
+        for (int c = threadIdx.x; c < nch; c += blockDim.x) {
+            const u32x4_t v = x[(size_t)t * nch + c];
 #pragma unroll
             for (int j = 0; j < MOE_MAX_TOPK; ++j)
                 if ((unsigned)at[j] < (unsigned)P)
-                    store_row16<THROUGH>(v, rows + (size_t)at[j] * bytes, bytes, c);
+                    __builtin_nontemporal_store(v, rows + (size_t)at[j] * nch + c);
             for (int i = 0; i < n_shared; ++i)
-                store_row16<THROUGH>(v, rows + ((size_t)P + (size_t)i * T + t) * bytes, bytes, c);
+                __builtin_nontemporal_store(v, rows + ((size_t)P + (size_t)i * T + t) * nch + c);
         }
         for (int c = threadIdx.x; c < nsc; c += blockDim.x) {
             const float v = x_scale[(size_t)t * nsc + c];
@@ -72,36 +67,43 @@ __global__ __launch_bounds__(1024) void dispatch_kernel(const char* __restrict__
     }
 }
 
+// Values that a lane takes at a time where rows of two types meet.
+template <class A, class B>
+constexpr int kShared = 16 / (sizeof(A) > sizeof(B) ? sizeof(A) : sizeof(B));
+
 template <class Tin, class Tout, bool NT>
 __global__ __launch_bounds__(1024) void dispatch_backward_kernel(const Tin* __restrict__ d_rows,
                                                                      const int32_t* __restrict__ unpermute,
                                                                      int T, int k, int H, int n_shared,
                                                                      Tout* __restrict__ dx)
 {
-    const int P = T * k, nch = H >> 3;
+    constexpr int V = kShared<Tin, Tout>;
+    const int P = T * k, nch = H / V;
     for (int t = blockIdx.x; t < T; t += gridDim.x) {
         int at[MOE_MAX_TOPK];
 #pragma unroll
         for (int j = 0; j < MOE_MAX_TOPK; ++j) at[j] = j < k ? unpermute[(size_t)t * k + j] : -1;
         for (int c = threadIdx.x; c < nch; c += blockDim.x) {
-            Raw8<Tin> v[MOE_MAX_TOPK];
+            Raw<Tin, V> v[MOE_MAX_TOPK];
 #pragma unroll
             for (int j = 0; j < MOE_MAX_TOPK; ++j) {
                 v[j].zero();
-                if ((unsigned)at[j] < (unsigned)P) v[j].template load<NT>(d_rows + (size_t)at[j] * H + 8 * c);
+                if ((unsigned)at[j] < (unsigned)P) v[j].template load<NT>(d_rows + (size_t)at[j] * H + V * c);
             }
-            float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            float a[V] = {};
 #pragma unroll
             for (int j = 0; j < MOE_MAX_TOPK; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) a[e] += v[j][e];
+                for (int e = 0; e < V; ++e) a[e] += v[j][e];
             for (int i = 0; i < n_shared; ++i) {
-                Raw8<Tin> b;
-                b.template load<NT>(d_rows + ((size_t)P + (size_t)i * T + t) * H + 8 * c);
+                Raw<Tin, V> b;
+                b.template load<NT>(d_rows + ((size_t)P + (size_t)i * T + t) * H + V * c);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) a[e] += b[e];
+                for (int e = 0; e < V; ++e) a[e] += b[e];
             }
-            store8_f32(dx + (size_t)t * H + 8 * c, a);
+            Raw<Tout, V> w;
+            w.set(a);
+            w.store(dx + (size_t)t * H + V * c);
         }
     }
 }
@@ -116,7 +118,8 @@ __global__ __launch_bounds__(1024) void finalize_backward_kernel(const Ty* __res
                                                                      float* __restrict__ d_scales)
 {
     __shared__ float s_dot[16][MOE_MAX_TOPK];
-    const int P = Tn * k, nch = H >> 3;
+    constexpr int V = kShared<Ty, T>;
+    const int P = Tn * k, nch = H / V;
     for (int t = blockIdx.x; t < Tn; t += gridDim.x) {
         int at[MOE_MAX_TOPK];
         float sc[MOE_MAX_TOPK], dot[MOE_MAX_TOPK];
@@ -127,33 +130,33 @@ __global__ __launch_bounds__(1024) void finalize_backward_kernel(const Ty* __res
             dot[j] = 0.0f;
         }
         for (int c = threadIdx.x; c < nch; c += blockDim.x) {
-            Raw8<Ty> g;
-            g.template load<NT>(dy + (size_t)t * H + 8 * c);
-            Raw8<T> v[MOE_MAX_TOPK];
+            Raw<Ty, V> g;
+            g.template load<NT>(dy + (size_t)t * H + V * c);
+            Raw<T, V> v[MOE_MAX_TOPK];
 #pragma unroll
             for (int j = 0; j < MOE_MAX_TOPK; ++j)
-                if ((unsigned)at[j] < (unsigned)P) v[j].template load<NT>(fc2 + (size_t)at[j] * H + 8 * c);
+                if ((unsigned)at[j] < (unsigned)P) v[j].template load<NT>(fc2 + (size_t)at[j] * H + V * c);
 #pragma unroll
             for (int j = 0; j < MOE_MAX_TOPK; ++j) {
                 if ((unsigned)at[j] >= (unsigned)P) continue;
-                float o[8];
+                float o[V];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
+                for (int e = 0; e < V; ++e) {
                     dot[j] += g[e] * v[j][e];
                     o[e] = sc[j] * g[e];
                 }
-                Raw8<T> w;
+                Raw<T, V> w;
                 w.set(o);
-                w.template store<NT>(d_fc2 + (size_t)at[j] * H + 8 * c);
+                w.template store<NT>(d_fc2 + (size_t)at[j] * H + V * c);
             }
             if (n_shared > 0) {
-                float o[8];
+                float o[V];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = g[e];
-                Raw8<T> w;
+                for (int e = 0; e < V; ++e) o[e] = g[e];
+                Raw<T, V> w;
                 w.set(o);
                 for (int i = 0; i < n_shared; ++i)
-                    w.template store<NT>(d_fc2 + ((size_t)P + (size_t)i * Tn + t) * H + 8 * c);
+                    w.template store<NT>(d_fc2 + ((size_t)P + (size_t)i * Tn + t) * H + V * c);
             }
         }
 #pragma unroll
@@ -177,14 +180,12 @@ __global__ __launch_bounds__(1024) void finalize_backward_kernel(const Ty* __res
 moe_status launch_dispatch(const void* x, const float* x_scale, int dt, int T, int H, int k, int n_shared,
                            const int32_t* unpermute, void* rows, float* rows_scale, hipStream_t s)
 {
-    const unsigned bytes = (unsigned)H * (dt == MOE_F32 ? 4 : dt == MOE_BF16 ? 2 : 1);
-    const bool through = (long)T * (k + n_shared + 1) * bytes > kStream;
-    auto* kernel = through ? dispatch_kernel<true> : dispatch_kernel<false>;
+    const int nch = (int)((size_t)H * (dt == MOE_F32 ? 4 : dt == MOE_BF16 ? 2 : 1) / 16);
     {
         TimedLaunch tl(MOE_KID_DISPATCH, s);
-        hipLaunchKernelGGL(kernel, dim3(std::min(T, kMaxGrid)), dim3(threads_for(bytes / 16)), 0, s,
-                           static_cast<const char*>(x), x_scale, T, k, n_shared, bytes,
-                           dt == MOE_FP8_E4M3 ? H / 128 : 0, unpermute, static_cast<char*>(rows), rows_scale);
+        hipLaunchKernelGGL(dispatch_kernel, dim3(std::min(T, kMaxGrid)), dim3(threads_for(nch, k > 2)), 0, s,
+                           static_cast<const u32x4_t*>(x), x_scale, T, k, n_shared, nch,
+                           dt == MOE_FP8_E4M3 ? H / 128 : 0, unpermute, static_cast<u32x4_t*>(rows), rows_scale);
     }
     return launch_status("dispatch_kernel");
 }
@@ -198,7 +199,7 @@ void launch_sum(const void* d_rows, const int32_t* unpermute, int T, int k, int 
     const bool nt = (long)T * (k + n_shared + 1) * H * (long)sizeof(Tin) > kStream;
     auto* kernel = nt ? dispatch_backward_kernel<Tin, Tout, true> : dispatch_backward_kernel<Tin, Tout, false>;
     TimedLaunch tl(MOE_KID_DISPATCH_BWD, s);
-    hipLaunchKernelGGL(kernel, dim3(std::min(T, kMaxGrid)), dim3(threads_for(H / 8)), 0, s,
+    hipLaunchKernelGGL(kernel, dim3(std::min(T, kMaxGrid)), dim3(threads_for(H / kShared<Tin, Tout>, k > 2)), 0, s,
                        static_cast<const Tin*>(d_rows), unpermute, T, k, H, n_shared, static_cast<Tout*>(dx));
 }
 
@@ -207,9 +208,10 @@ void launch_fin(const void* dy, const void* fc2, const int32_t* unpermute, const
                 int H, int n_shared, void* d_fc2, float* d_scales, hipStream_t s)
 {
     const bool nt = (long)Tn * (2 * (k + n_shared) + 1) * H * (long)sizeof(T) > kStream;
+    const bool wide = k > 4 && (nt || Tn < device_cu_count());
     auto* kernel = nt ? finalize_backward_kernel<Ty, T, true> : finalize_backward_kernel<Ty, T, false>;
     TimedLaunch tl(MOE_KID_FINALIZE_BWD, s);
-    hipLaunchKernelGGL(kernel, dim3(std::min(Tn, kMaxGrid)), dim3(threads_for(H / 8)), 0, s,
+    hipLaunchKernelGGL(kernel, dim3(std::min(Tn, kMaxGrid)), dim3(threads_for(H / kShared<Ty, T>, wide)), 0, s,
                        static_cast<const Ty*>(dy), static_cast<const T*>(fc2), unpermute, scales, Tn, k, H,
                        n_shared, static_cast<T*>(d_fc2), d_scales);
 }

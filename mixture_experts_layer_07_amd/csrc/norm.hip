@@ -52,23 +52,32 @@ __device__ __forceinline__ void row_sum(float (&v)[N], float (*s)[kMaxWaves][N],
     }
 }
 
+template <int V>
+__device__ __forceinline__ void store_f32(float* p, const float (&v)[V])
+{
+#pragma unroll
+    for (int i = 0; i < V; i += 4)
+        *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+
 // No __restrict__: total and y may be x or residual.
 template <class T, int NV, bool WAVE, bool NT>
 __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const T* x, const T* residual, const T* weight,
                                                        int rows, int H, float eps, T* total, T* y,
                                                        uint8_t* yq, float* y_scale)
 {
+    constexpr int V = Raw<T>::kValues;
     __shared__ float s_sum[2][kMaxWaves][1];
     int buf = 0;
     const int tid = WAVE ? (threadIdx.x & 63) : threadIdx.x;
     const int stride = WAVE ? 64 : blockDim.x;
     const int per = WAVE ? (blockDim.x >> 6) : 1;  // rows a workgroup takes at a time
-    const int nch = H >> 3;
+    const int nch = H / V;
     const float inv = 1.0f / (float)H;
     for (long row = (long)blockIdx.x * per + (WAVE ? threadIdx.x >> 6 : 0); row < rows;
          row += (long)gridDim.x * per) {
         const size_t r0 = (size_t)row * H;
-        Raw8<T> a[NV], b[NV], w[NV];
+        Raw<T> a[NV], b[NV], w[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * stride;
@@ -76,43 +85,44 @@ __global__ __launch_bounds__(WAVE ? 256 : 1024) void rmsnorm_kernel(const T* x, 
             b[i].zero();
             w[i].zero();
             if (c < nch) {
-                a[i].template load<NT>(x + r0 + 8 * c);
-                if (residual) b[i].template load<NT>(residual + r0 + 8 * c);
-                w[i].load(weight + 8 * c);
+                a[i].template load<NT>(x + r0 + V * c);
+                if (residual) b[i].template load<NT>(residual + r0 + V * c);
+                w[i].load(weight + V * c);
             }
         }
         float sum[1] = {0.0f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             if (residual) {
-                float z[8];
+                float z[V];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) z[e] = a[i][e] + b[i][e];
+                for (int e = 0; e < V; ++e) z[e] = a[i][e] + b[i][e];
                 a[i].set(z);  // the norm is taken of the stored sum
                 const int c = tid + i * stride;
-                if (c < nch) a[i].template store<NT>(total + r0 + 8 * c);
+                if (c < nch) a[i].template store<NT>(total + r0 + V * c);
             }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sum[0] += a[i][e] * a[i][e];
+            for (int e = 0; e < V; ++e) sum[0] += a[i][e] * a[i][e];
         }
         row_sum<WAVE, 1>(sum, s_sum, buf);
         const float cn = rsqrtf(sum[0] * inv + eps);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * stride;
-            float v[8];
+            float v[V];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = a[i][e] * cn * w[i][e];
+            for (int e = 0; e < V; ++e) v[e] = a[i][e] * cn * w[i][e];
             if (y && c < nch) {
-                Raw8<T> o;
+                Raw<T> o;
                 o.set(v);
-                o.template store<NT>(y + r0 + 8 * c);
+                o.template store<NT>(y + r0 + V * c);
             }
-            if (yq) {  // H is a multiple of 128: the 16 lanes of a block are in or out together
-                const float s = max16(absmax8(v)) / 448.0f;
+            if (yq) {  // H is a multiple of 128: the lanes of a block are in or out together
+                constexpr int kLanes = 128 / V;
+                const float s = block_absmax(v) / 448.0f;
                 if (c < nch) {
-                    *reinterpret_cast<uint2*>(yq + r0 + 8 * c) = fp8x8_code(v, s);
-                    if ((c & 15) == 0) y_scale[(r0 >> 7) + (c >> 4)] = s;
+                    store_codes(v, s, yq + r0 + V * c);
+                    if ((c & (kLanes - 1)) == 0) y_scale[(r0 >> 7) + c / kLanes] = s;
                 }
             }
         }
@@ -127,29 +137,30 @@ __global__ __launch_bounds__(!WAVE ? 512 : NV == 4 ? 256 : 1024) void rmsnorm_ba
     const T* dy, const T* z, const T* weight, const T* dtotal, int rows, int H, float eps, T* dz,
     float* __restrict__ part)
 {
+    constexpr int V = Raw<T>::kValues;
     constexpr bool kAhead = WAVE && NV == 1;
     __shared__ float s_sum[2][kMaxWaves][2];
     constexpr int kAdd = NV == 4 ? 4 : 8;  // waves whose sums are in LDS together
-    __shared__ float s_dw[WAVE ? kAdd : 1][WAVE ? 512 * NV : 1];
+    __shared__ float s_dw[WAVE ? kAdd : 1][WAVE ? 64 * NV * V : 1];
     int buf = 0;
     const int wave = threadIdx.x >> 6;
     const int tid = WAVE ? (threadIdx.x & 63) : threadIdx.x;
     const int stride = WAVE ? 64 : blockDim.x;
     const int per = WAVE ? (blockDim.x >> 6) : 1;
-    const int nch = H >> 3;
+    const int nch = H / V;
     const float inv = 1.0f / (float)H;
     struct Row {
-        Raw8<T> z[NV], g[NV], d[NV];
+        Raw<T> z[NV], g[NV], d[NV];
     };
-    Raw8<T> w[NV];
-    float dw[NV][8];
+    Raw<T> w[NV];
+    float dw[NV][V];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int c = tid + i * stride;
         w[i].zero();
-        if (c < nch) w[i].load(weight + 8 * c);
+        if (c < nch) w[i].load(weight + V * c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+        for (int e = 0; e < V; ++e) dw[i][e] = 0.0f;
     }
     const long step = (long)gridDim.x * per;
     auto fetch = [&](Row& r, long row) {
@@ -161,9 +172,9 @@ __global__ __launch_bounds__(!WAVE ? 512 : NV == 4 ? 256 : 1024) void rmsnorm_ba
             r.g[i].zero();
             r.d[i].zero();
             if (c < nch && row < rows) {
-                r.z[i].template load<NT>(z + r0 + 8 * c);
-                r.g[i].template load<NT>(dy + r0 + 8 * c);
-                if (dtotal) r.d[i].template load<NT>(dtotal + r0 + 8 * c);
+                r.z[i].template load<NT>(z + r0 + V * c);
+                r.g[i].template load<NT>(dy + r0 + V * c);
+                if (dtotal) r.d[i].template load<NT>(dtotal + r0 + V * c);
             }
         }
     };
@@ -177,7 +188,7 @@ __global__ __launch_bounds__(!WAVE ? 512 : NV == 4 ? 256 : 1024) void rmsnorm_ba
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < V; ++e) {
                 sum[0] += cur.z[i][e] * cur.z[i][e];
                 sum[1] += cur.g[i][e] * w[i][e] * cur.z[i][e];
             }
@@ -187,34 +198,33 @@ __global__ __launch_bounds__(!WAVE ? 512 : NV == 4 ? 256 : 1024) void rmsnorm_ba
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * stride;
-            float v[8];
+            float v[V];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < V; ++e) {
                 const float n = cur.z[i][e] * cn;
                 v[e] = cn * (cur.g[i][e] * w[i][e] - n * mean) + cur.d[i][e];
                 dw[i][e] += cur.g[i][e] * n;
             }
             if (c < nch) {
-                Raw8<T> o;
+                Raw<T> o;
                 o.set(v);
-                o.template store<NT>(dz + (size_t)row * H + 8 * c);
+                o.template store<NT>(dz + (size_t)row * H + V * c);
             }
         }
         if constexpr (kAhead) cur = next;
     }
     float* out = part + (size_t)blockIdx.x * H;
     if constexpr (WAVE) {  // the waves' sums, added in order, kAdd waves at a time
-        float v[2 * NV];  // a 256-thread workgroup has up to 2 NV columns a thread
-#pragma unroll
-        for (int q = 0; q < 2 * NV; ++q) v[q] = 0.0f;
+        constexpr int kCols = NV * V / 4;  // columns a thread of a 256-thread workgroup has at most
+        float v[kCols] = {};
         for (int k0 = 0; k0 < per; k0 += kAdd) {
             if (wave >= k0 && wave < k0 + kAdd) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) store8_f32(&s_dw[wave - k0][8 * (tid + 64 * i)], dw[i]);
+                for (int i = 0; i < NV; ++i) store_f32(&s_dw[wave - k0][V * (tid + 64 * i)], dw[i]);
             }
             __syncthreads();
 #pragma unroll
-            for (int q = 0; q < 2 * NV; ++q) {
+            for (int q = 0; q < kCols; ++q) {
                 const int h = threadIdx.x + q * blockDim.x;
                 if (h < H)
                     for (int k = 0; k < min(kAdd, per - k0); ++k) v[q] += s_dw[k][h];
@@ -222,7 +232,7 @@ __global__ __launch_bounds__(!WAVE ? 512 : NV == 4 ? 256 : 1024) void rmsnorm_ba
             __syncthreads();
         }
 #pragma unroll
-        for (int q = 0; q < 2 * NV; ++q) {
+        for (int q = 0; q < kCols; ++q) {
             const int h = threadIdx.x + q * blockDim.x;
             if (h < H) out[h] = v[q];
         }
@@ -230,7 +240,7 @@ __global__ __launch_bounds__(!WAVE ? 512 : NV == 4 ? 256 : 1024) void rmsnorm_ba
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * stride;
-            if (c < nch) store8_f32(out + 8 * c, dw[i]);
+            if (c < nch) store_f32(out + V * c, dw[i]);
         }
     }
 }
@@ -268,23 +278,23 @@ struct Shape {
     int grid;
 };
 
-// The same for every T, so a row's result does not depend on how many rows
-// there are beside it.
-Shape forward_shape(int T, int H)
+// V: values of a chunk.  The same for every T, so a row's result does not
+// depend on how many rows there are beside it.
+Shape forward_shape(int T, int H, int V)
 {
-    const int nch = H / 8;
+    const int nch = H / V;
     Shape s;
     s.wave = nch <= 128;
-    s.nv = nch <= 64 ? 1 : 2;
-    s.threads = s.wave ? 256 : (nch + 127) / 128 * 64;
+    s.nv = nch <= 64 ? 1 : nch <= 2048 ? 2 : 4;
+    s.threads = s.wave ? 256 : (nch + 64 * s.nv - 1) / (64 * s.nv) * 64;
     s.per = s.wave ? 4 : 1;
     s.grid = std::min((T + s.per - 1) / s.per, 1 << 20);
     return s;
 }
 
-Shape backward_shape(int T, int H)
+Shape backward_shape(int T, int H, int V)
 {
-    const int nch = H / 8;
+    const int nch = H / V;
     Shape s;
     s.wave = nch <= 256;
     if (s.wave) {
@@ -292,7 +302,7 @@ Shape backward_shape(int T, int H)
         s.threads = T <= 64 && s.nv <= 2 ? 1024 : 256;
         s.per = s.threads / 64;
     } else {
-        s.nv = nch <= 512 ? 2 : 4;
+        s.nv = nch <= 512 ? 2 : nch <= 2048 ? 4 : 8;
         s.threads = nch <= 1024 ? 256 : 512;
         s.per = 1;
     }
@@ -328,18 +338,20 @@ void launch_bwd(const Shape& sh, const void* dy, const void* z, const void* weig
 
 size_t rmsnorm_backward_scratch_bytes(int T, int H)
 {
-    return (size_t)backward_shape(T, H).grid * H * sizeof(float);
+    // whatever the type
+    return (size_t)std::max(backward_shape(T, H, 4).grid, backward_shape(T, H, 8).grid) * H * sizeof(float);
 }
 
 moe_status launch_rmsnorm(const void* x, const void* residual, const void* weight, int dt, int T, int H,
                           float eps, void* total, void* y, uint8_t* yq, float* y_scale, hipStream_t s)
 {
-    const Shape sh = forward_shape(T, H);
+    const Shape sh = forward_shape(T, H, dt == MOE_F32 ? 4 : 8);
     {
         TimedLaunch tl(MOE_KID_RMSNORM, s);
         auto go = [&](auto type) {
             using V = decltype(type);
-            auto* f = !sh.wave ? launch_fwd<V, 2, false>
+            constexpr int kWide = sizeof(V) == 4 ? 4 : 2;  // rows of more than 2048 chunks are fp32
+            auto* f = !sh.wave ? (sh.nv == 2 ? launch_fwd<V, 2, false> : launch_fwd<V, kWide, false>)
                       : sh.nv == 1 ? launch_fwd<V, 1, true> : launch_fwd<V, 2, true>;
             f(sh, x, residual, weight, T, H, eps, total, y, yq, y_scale, s);
         };
@@ -353,14 +365,16 @@ moe_status launch_rmsnorm_backward(const void* dy, const void* z, const void* we
                                    int dt, int T, int H, float eps, void* dz, float* dweight, void* ws,
                                    hipStream_t s)
 {
-    const Shape sh = backward_shape(T, H);
+    const Shape sh = backward_shape(T, H, dt == MOE_F32 ? 4 : 8);
     // a single workgroup's sum is the answer
     float* part = T > 0 && sh.grid == 1 ? dweight : static_cast<float*>(ws);
     if (T > 0) {
         TimedLaunch tl(MOE_KID_RMSNORM_BWD, s);
         auto go = [&](auto type) {
             using V = decltype(type);
-            auto* f = !sh.wave ? (sh.nv == 2 ? launch_bwd<V, 2, false> : launch_bwd<V, 4, false>)
+            constexpr int kWide = sizeof(V) == 4 ? 8 : 4;  // rows of more than 2048 chunks are fp32
+            auto* f = !sh.wave ? (sh.nv == 2   ? launch_bwd<V, 2, false>
+                                  : sh.nv == 4 ? launch_bwd<V, 4, false> : launch_bwd<V, kWide, false>)
                       : sh.nv == 1 ? launch_bwd<V, 1, true>
                       : sh.nv == 2 ? launch_bwd<V, 2, true> : launch_bwd<V, 4, true>;
             f(sh, dy, z, weight, dtotal, T, H, eps, dz, part, s);

@@ -1,5 +1,5 @@
 // Device helpers of the row operators (norm, dispatch, activation and the
-// gradients): 8-value chunks of a row, sums over lanes, 1x128 e4m3 blocks.
+// gradients): 16-byte chunks of a row, sums over lanes, 1x128 e4m3 blocks.
 #pragma once
 
 #include "common.h"
@@ -17,54 +17,49 @@ namespace {
 // 156.2 us for the three) and loses nothing below.
 constexpr long kStream = 96l << 20;
 
-// 8 consecutive values of a row as raw 16-byte words (bf16: one, fp32: two),
-// widened to fp32 only where they are used.
-template <class T>
-struct Raw8 {
-    static constexpr int W = sizeof(T) / 2;
-    u32x4_t w[W];
+// V consecutive values of a row as raw words, widened to fp32 only where they
+// are used.  A lane takes 16 bytes at a time, 8 bf16 or 4 fp32 values, so that
+// a wave's access is one contiguous kilobyte (8 fp32 values a lane made each
+// store half lines: swiglu_backward of 16384 x 2048 fp32 160 us against 106
+// without the hint).  Where bf16 and fp32 rows meet, both take 4 values.
+template <class T, int V = 16 / (int)sizeof(T)>
+struct Raw {
+    static constexpr int kValues = V, W = V * (int)sizeof(T) / 4;
+    typedef uint32_t words_t __attribute__((ext_vector_type(W)));
+    words_t w;
     template <bool NT = false>
     __device__ __forceinline__ void load(const T* p)
     {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            const u32x4_t* q = reinterpret_cast<const u32x4_t*>(reinterpret_cast<const char*>(p) + 16 * i);
-            w[i] = NT ? __builtin_nontemporal_load(q) : *q;
-        }
+        const words_t* q = reinterpret_cast<const words_t*>(p);
+        if constexpr (NT) w = __builtin_nontemporal_load(q);
+        else w = *q;
     }
-    __device__ __forceinline__ void zero()
-    {
-#pragma unroll
-        for (int i = 0; i < W; ++i) w[i] = u32x4_t{0, 0, 0, 0};
-    }
+    __device__ __forceinline__ void zero() { w = words_t(0u); }
     __device__ __forceinline__ float operator[](int i) const
     {
-        if constexpr (W == 1) {
-            const uint32_t u = w[0][i >> 1];
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t u = w[i >> 1];
             return __uint_as_float((i & 1) ? (u & 0xffff0000u) : (u << 16));
         } else {
-            return __uint_as_float(w[i >> 2][i & 3]);
+            return __uint_as_float(w[i]);
         }
     }
-    __device__ __forceinline__ void set(const float v[8])
+    __device__ __forceinline__ void set(const float (&v)[V])
     {
-        if constexpr (W == 1) {
+        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[0][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            for (int i = 0; i < W; ++i) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i >> 2][i & 3] = __float_as_uint(v[i]);
+            for (int i = 0; i < V; ++i) w[i] = __float_as_uint(v[i]);
         }
     }
     template <bool NT = false>
     __device__ __forceinline__ void store(T* p) const
     {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-            u32x4_t* q = reinterpret_cast<u32x4_t*>(reinterpret_cast<char*>(p) + 16 * i);
-            if constexpr (NT) __builtin_nontemporal_store(w[i], q);
-            else *q = w[i];
-        }
+        words_t* q = reinterpret_cast<words_t*>(p);
+        if constexpr (NT) __builtin_nontemporal_store(w, q);
+        else *q = w;
     }
 };
 
@@ -102,11 +97,15 @@ __device__ __forceinline__ float wave_sum_f32(float v)
     return v;
 }
 
-__device__ __forceinline__ float absmax8(const float v[8])
+// Maximum of |v| over a 1x128 block, V values a lane: 128 / V consecutive lanes.
+template <int V>
+__device__ __forceinline__ float block_absmax(const float (&v)[V])
 {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+    for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(v[i]));
+    m = max16(m);
+    if constexpr (V == 4) m = fmaxf(m, __shfl_xor(m, 16, 64));
     return m;
 }
 
@@ -123,38 +122,45 @@ __device__ __forceinline__ float quotient(float v, float s, float r)
     return __builtin_copysignf(q, v);
 }
 
-// Eight values -> their e4m3 codes with block scale s = fl32(amax / 448), the
-// codes that fp8x4_code gives (fl32(v / s) rounded to nearest even).  One
+// V values -> their e4m3 codes with block scale s = fl32(amax / 448), stored at
+// q: the codes that fp8x4_code gives (fl32(v / s) rounded to nearest even).  One
 // reciprocal a block instead of a division a value, where no residual can
 // underflow (s >= 2^-60: a value that does not round to zero has |v| >= 2^-70,
 // so its residual is a multiple of 2^-118) and nothing overflows; the quotient
-// is then at most 448 (1 + 2^-23), which needs no clamp.  The activation with
-// its checkpoint: 222 -> 219 us alone, 222 -> 188 us with the narrow
-// workgroups and hinted stores of swiglu.hip.
-__device__ __forceinline__ uint2 fp8x8_code(const float v[8], float s)
+// is then at most 448 (1 + 2^-23), which needs no clamp.  swiglu with a
+// checkpoint of 73728 x 2048: 226 -> 219 us.
+template <int V>
+__device__ __forceinline__ void store_codes(const float (&v)[V], float s, uint8_t* q)
 {
+    typedef uint32_t words_t __attribute__((ext_vector_type(V / 4)));
+    words_t w;
     if (s >= 0x1p-60f && s <= 0x1p+100f) {
         const float r = 1.0f / s;
-        float q[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = quotient(v[i], s, r);
-        int lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
-        lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
-        int hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
-        hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[6], q[7], hi, true);
-        return make_uint2((uint32_t)lo, (uint32_t)hi);
+        for (int i = 0; i < V / 4; ++i) {
+            int c = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[4 * i], s, r), quotient(v[4 * i + 1], s, r), 0, false);
+            c = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[4 * i + 2], s, r), quotient(v[4 * i + 3], s, r), c, true);
+            w[i] = (uint32_t)c;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V / 4; ++i) {
+            const float f[4] = {v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+            w[i] = fp8x4_code(f, s);
+        }
     }
-    const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
-    return make_uint2(fp8x4_code(lo, s), fp8x4_code(hi, s));
+    *reinterpret_cast<words_t*>(q) = w;
 }
 
-// v = code * scale of eight e4m3 codes.
-__device__ __forceinline__ void fp8x8_value(uint2 q, float s, float v[8])
+// v = code * scale of the V e4m3 codes at q.
+template <int V>
+__device__ __forceinline__ void load_codes(const uint8_t* q, float s, float (&v)[V])
 {
+    typedef uint32_t words_t __attribute__((ext_vector_type(V / 4)));
     typedef float f32x2_t __attribute__((ext_vector_type(2)));
-    const uint32_t w[2] = {q.x, q.y};
+    const words_t w = *reinterpret_cast<const words_t*>(q);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < V / 4; ++i) {
         const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false);
         const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
         v[4 * i] = a.x * s;

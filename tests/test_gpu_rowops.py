@@ -177,11 +177,10 @@ def test_rmsnorm_special_rows(dt):
 
 
 def dweight_depth(T, H):
-    """Additions in the longest chain of dweight: a partial sum's rows (4 in a row at least before the
-    rows are spread over up to 512 sums of 4 waves), its waves (4, or 16 that then are all), the 16
-    partial sums of a run, 32 runs."""
-    per = 4 if H <= 2048 else 1
-    return -(-T // (512 * per)) + 4 + 16 + 32
+    """Additions in the longest chain of dweight: a partial sum's rows (spread over up to 512 sums, or
+    all of 4 where one workgroup takes them), its waves (4, or 16 that then are all), the 16 partial
+    sums of a run, 32 runs."""
+    return -(-T // 512) + 4 + 16 + 32
 
 
 @pytest.mark.parametrize("dt", TYPES)
