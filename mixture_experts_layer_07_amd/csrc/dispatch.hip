@@ -24,10 +24,10 @@ constexpr int kMaxGrid = 1 << 20;
 // rows a token the whole row at once is what the memory likes best; with few, a
 // workgroup of 1024 threads waits too long for too little.  512 / 1024 threads:
 //   dispatch and gradient, 4096 x 7168 bf16  k = 1 47 / 64 us, k = 2 65 / 74 us,
-//     k = 4 110 / 105 us; 8192 tokens, k = 8 and a shared expert 463 / 446 us
+//     k = 4 110 / 105 us; 8192 tokens, k = 8 and a shared expert 452 / 439 us
 //   finalize_backward, 4096 x 7168 bf16  k = 1 34 / 52 us, k = 2 53 / 63 us, k = 4
-//     96.5 / 97.0 us, k = 6 142 / 140 us; 512 tokens, k = 8 25.8 / 27.7 us; 64 x
-//     7168 fp32, k = 8 12.9 / 10.8 us
+//     96.5 / 97.0 us, k = 6 142 / 140 us, 8192 tokens, k = 8 and a shared expert 396 /
+//     385 us; 512 tokens, k = 8 25.8 / 27.7 us; 64 x 7168 fp32, k = 8 12.9 / 10.8 us
 int threads_for(int n, bool wide) { return std::min(wide ? 1024 : 512, (n + 63) / 64 * 64); }
 
 // Rows of nch 16-byte words; with scales, nsc floats a row.  A row is written

@@ -8,15 +8,15 @@
 // rows, a workgroup owns a row; a thread holds NV chunks of 8 consecutive
 // values at chunk indices tid, tid + stride, ...
 //
-// Measured on MI355X (8192 x 7168 bf16, a copy moves 5.1-6.5 TB/s):
+// Measured on MI355X (8192 x 7168 bf16; a copy moves 5.1 TB/s, 6.5 at best):
 //   forward with residual, y and codes  84 us, 6.3 TB/s.  Two chunks a thread:
-//     one 91 us, four 85 us; without the streaming hints 94.6 us.
+//     one 91 us, four 85 us.
 //   backward with dtotal  84 us, 5.6 TB/s (the kernel 79 us, the sum of the
 //     partial rows 5 us).  256 or 1024 partial rows instead of 512: 104 / 90 us;
 //     two chunks a thread 85 us, one 104 us; the next row's loads in flight over
 //     the reduction 85-105 us (registers), kept only where a row is a chunk a
 //     lane.
-//   one token 5 us a call, 63 x 256 fp32 backward 7 us: launches.
+//   one token 5.0 us a call, the gradients of 63 x 256 fp32 5.2 us: launches.
 #include <algorithm>
 
 #include "rowops.h"

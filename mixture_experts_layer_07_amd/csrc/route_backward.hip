@@ -11,7 +11,9 @@
 // The products of the difference are rounded alike (no fused multiply-add):
 // one renormalised weight alone, which is constant, has gradient exactly 0.
 //
-// Latency-bound while small, then bound by the writes (T*E floats).  A wave
+// Latency-bound while small (8192 x 256, k = 8: 5.0 us a call), then bound by
+// the writes and by the lines that the kept logits are gathered from (65536 x
+// 256: 24 us; plain softmax 36 us).  A wave
 // owns eight tokens, eight lanes each: they compute the kept experts' gradients
 // (an exponential and three divisions each; sums over a token's lanes by lane
 // permutations) and put them into a tile of the output in LDS, which then goes

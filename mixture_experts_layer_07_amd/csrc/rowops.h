@@ -9,12 +9,13 @@ namespace {
 
 // Calls that move more bytes than this stream past the caches: loads and
 // stores carry the non-temporal hint (template argument NT).  Plain / hinted,
-// inputs and outputs of three calls in turn: rmsnorm 66 MB 11.7 / 14.3 us, 132
-// MB 28.6 / 26.1 us, 528 MB 94.6 / 84.4 us; finalize_backward 84 MB 16.6 / 20.1
-// us, 125 MB 30.9 / 27.4 us, 1.0 GB 104.6 / 96.0 us; swiglu_backward 170 MB
-// 60.0 / 55.7 us with its forward call.  With a producer before it and a
-// quantiser that reads y after it, rmsnorm gains as well at 528 MB (165.6 ->
-// 156.2 us for the three) and loses nothing below.
+// the inputs and outputs of three calls in turn:
+//   rmsnorm            66 MB 11.9 / 14.4 us   132 MB 28.6 / 26.1   528 MB 93.9 / 84.2
+//   its gradients      59 MB 17.6 / 19.1      235 MB 52.7 / 47.2   470 MB 94.3 / 84.1
+//   finalize_backward  62 MB 12.2 / 13.7      125 MB 28.2 / 27.4   2.1 GB 410 / 385
+//   swiglu + gradient  152 MB 32.4 / 26.3     304 MB 56.1 / 51.5   2.7 GB 466 / 460
+// With a producer of x before it and a quantiser that reads y after it, rmsnorm
+// gains as well at 528 MB (165.6 -> 156.2 us for the three).
 constexpr long kStream = 96l << 20;
 
 // V consecutive values of a row as raw words, widened to fp32 only where they
@@ -128,7 +129,7 @@ __device__ __forceinline__ float quotient(float v, float s, float r)
 // underflow (s >= 2^-60: a value that does not round to zero has |v| >= 2^-70,
 // so its residual is a multiple of 2^-118) and nothing overflows; the quotient
 // is then at most 448 (1 + 2^-23), which needs no clamp.  swiglu with a
-// checkpoint of 73728 x 2048: 226 -> 219 us.
+// checkpoint of 73728 x 2048: 210 -> 191 us against a division a value.
 template <int V>
 __device__ __forceinline__ void store_codes(const float (&v)[V], float s, uint8_t* q)
 {

@@ -9,11 +9,11 @@
 // a step; the stride's whole rows and rest come from the host, so no division
 // is made in the loop.
 //
-// Measured on MI355X, 73728 x 2048 bf16: forward with the checkpoint 190 us (1.22
-// GB, 6.4 TB/s), backward with h again 270 us (1.52 GB, 5.6 TB/s), 458-465 us for
-// the two.  64, 128, 256 threads a workgroup 458, 457, 471 us (4096 rows with
-// codes of h alone 9.2, 9.1, 9.3 us); two or four chunks a thread in flight 470,
-// 494 us; 32 bytes a lane in the backward 590 us (half lines a store).
+// Measured on MI355X, 73728 x 2048 bf16: forward with the checkpoint 191 us (1.22
+// GB, 6.4 TB/s), backward with h again 270 us (1.52 GB, 5.6 TB/s), 460 us for the
+// two; 4096 rows to codes of h 8.9 us.  64, 128, 256 threads a workgroup 457, 460,
+// 475 us; two or four chunks a thread in flight 470, 494 us; 32 bytes a lane in the
+// backward 590 us (half lines a store).
 #include <algorithm>
 
 #include "rowops.h"
