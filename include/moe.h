@@ -335,7 +335,7 @@ moe_status moe_expert_ffn_fp8_fused(const uint8_t* xq, const float* x_scale, int
  *    (MOE_ERR_INVALID_ARG otherwise); the others need only their element's
  *    alignment.
  *  - An output may not overlap an input or another output except where the
- *    call says so.
+ *    call says so (the same pointer is refused, a partial overlap is not seen).
  *  - Rows are independent: a NaN or infinity in one row changes no other row
  *    (dweight, which sums over the rows, excepted).
  */
@@ -410,7 +410,10 @@ size_t moe_rmsnorm_backward_workspace_size(int T, int H);
  *             write them.
  *  H          a multiple of 8 (fp8: of 128), at most 2^28.
  *  unpermute  device int32 [T*k] from moe_permute.  A pair whose entry lies
- *             outside [0, T*k) is dropped: no row is written for it.
+ *             outside [0, T*k) is dropped: no row is written for it.  (The
+ *             gradients below skip such pairs too; moe_finalize does not, it
+ *             needs every entry valid.)  Two pairs with the same entry give
+ *             unspecified contents of that row.
  *  rows       device [T*k + n_shared*T, H] in `dt` out.  Rows that no pair
  *             names are left as they were.
  *  rows_scale device fp32 [T*k + n_shared*T, H/128] out for MOE_FP8_E4M3,

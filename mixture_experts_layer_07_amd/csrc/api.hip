@@ -416,6 +416,20 @@ static bool aligned16(std::initializer_list<const void*> ps)
     return (bits & 15) == 0;
 }
 
+// Whether an output is one of these buffers (partial overlaps are the caller's
+// to avoid).
+static bool is_any(const void* out, std::initializer_list<const void*> ps)
+{
+    for (const void* p : ps)
+        if (out && out == p) return true;
+    return false;
+}
+
+static moe_status same_buffer()
+{
+    return set_error(MOE_ERR_INVALID_ARG, "an output is the same buffer as an input or another output");
+}
+
 static moe_status misaligned()
 {
     return set_error(MOE_ERR_INVALID_ARG, "[rows, columns] buffers must be 16-byte aligned");
@@ -453,7 +467,9 @@ moe_status moe_rmsnorm(const void* x, const void* residual, const void* weight, 
         return set_error(MOE_ERR_INVALID_ARG, "residual and total must be given together or not at all");
     if (!yq != !y_scale) return set_error(MOE_ERR_INVALID_ARG, "yq and y_scale must be given together or not at all");
     if (!y && !yq) return set_error(MOE_ERR_INVALID_ARG, "y or yq must be given");
-    if (y && y == total) return set_error(MOE_ERR_INVALID_ARG, "y and total must be different buffers");
+    if (is_any(y, {total, residual, weight, yq, y_scale}) || is_any(total, {weight, yq, y_scale}) ||
+        is_any(yq, {x, residual, weight, y_scale}) || is_any(y_scale, {x, residual, weight}))
+        return same_buffer();
     if (yq && H % 128) return set_error(MOE_ERR_UNSUPPORTED, "H must be a multiple of 128 with yq (got %d)", H);
     if (!aligned16({x, residual, weight, total, y, yq})) return misaligned();
     return launch_rmsnorm(x, residual, weight, dt, T, H, eps, total, y, yq, y_scale,
@@ -476,6 +492,9 @@ moe_status moe_rmsnorm_backward(const void* dy, const void* z, const void* weigh
     if (T > 0) {
         if (!dy || !z || !weight || !dz)
             return set_error(MOE_ERR_INVALID_ARG, "dy, z, weight and dz must be non-null");
+        if (is_any(dz, {z, weight, dweight, ws}) || is_any(dweight, {dy, z, weight, dtotal, ws}) ||
+            is_any(ws, {dy, z, weight, dtotal}))
+            return same_buffer();
         if (!aligned16({dy, z, weight, dtotal, dz, dweight, ws})) return misaligned();
         const size_t need = rmsnorm_backward_scratch_bytes(T, H);
         if (!ws || ws_bytes < need)
@@ -514,6 +533,8 @@ moe_status moe_dispatch(const void* x, const float* x_scale, int dt, int T, int 
     if (!x || !unpermute || !rows) return set_error(MOE_ERR_INVALID_ARG, "x, unpermute and rows must be non-null");
     if (dt == MOE_FP8_E4M3 ? !x_scale || !rows_scale : x_scale || rows_scale)
         return set_error(MOE_ERR_INVALID_ARG, "x_scale and rows_scale go with fp8 rows, and only with them");
+    if (is_any(rows, {x, x_scale, unpermute, rows_scale}) || is_any(rows_scale, {x, x_scale, unpermute}))
+        return same_buffer();
     if (!aligned16({x, rows})) return misaligned();
     return launch_dispatch(x, x_scale, dt, T, H, k, n_shared, unpermute, rows, rows_scale,
                            static_cast<hipStream_t>(stream));
@@ -529,6 +550,7 @@ moe_status moe_dispatch_backward(const void* d_rows, int dt, const int32_t* unpe
     if (T == 0) return MOE_OK;
     if (!d_rows || !unpermute || !dx)
         return set_error(MOE_ERR_INVALID_ARG, "d_rows, unpermute and dx must be non-null");
+    if (is_any(dx, {d_rows, unpermute})) return same_buffer();
     if (!aligned16({d_rows, dx})) return misaligned();
     return launch_dispatch_backward(d_rows, dt, unpermute, T, k, H, n_shared, dx, dxt,
                                     static_cast<hipStream_t>(stream));
@@ -545,6 +567,8 @@ moe_status moe_finalize_backward(const void* dy, int dyt, const void* fc2_out, i
     if (T == 0) return MOE_OK;
     if (!dy || !fc2_out || !unpermute || !scales || !d_fc2 || !d_scales)
         return set_error(MOE_ERR_INVALID_ARG, "dy, fc2_out, unpermute, scales, d_fc2 and d_scales must be non-null");
+    if (is_any(d_fc2, {dy, unpermute, scales, d_scales}) || is_any(d_scales, {dy, fc2_out, unpermute, scales}))
+        return same_buffer();
     if (!aligned16({dy, fc2_out, d_fc2})) return misaligned();
     return launch_finalize_backward(dy, dyt, fc2_out, dt, unpermute, scales, T, k, H, n_shared, d_fc2, d_scales,
                                     static_cast<hipStream_t>(stream));
@@ -566,6 +590,7 @@ moe_status moe_route_backward(const float* logits, const int32_t* ids, const flo
     if (T == 0) return MOE_OK;
     if (!logits || !ids || !d_scales || !d_logits)
         return set_error(MOE_ERR_INVALID_ARG, "logits, ids, d_scales and d_logits must be non-null");
+    if (is_any(d_logits, {logits, ids, d_scales})) return same_buffer();
     if (!aligned16({d_logits})) return set_error(MOE_ERR_INVALID_ARG, "d_logits must be 16-byte aligned");
     return launch_route_backward(logits, ids, d_scales, T, E, method, k, scaling, flags, d_logits,
                                  static_cast<hipStream_t>(stream));
@@ -593,6 +618,9 @@ moe_status moe_swiglu(const void* gu, int dt, int rows, int I, void* h, uint8_t*
     if (!h && !hq) return set_error(MOE_ERR_INVALID_ARG, "h or hq must be given");
     if (!hq != !h_scale || !guq != !gu_scale)
         return set_error(MOE_ERR_INVALID_ARG, "codes and their scales must be given together or not at all");
+    if (is_any(gu, {h, hq, h_scale, guq, gu_scale}) || is_any(h, {hq, h_scale, guq, gu_scale}) ||
+        is_any(hq, {h_scale, guq, gu_scale}) || is_any(h_scale, {guq, gu_scale}) || is_any(guq, {gu_scale}))
+        return same_buffer();
     if (!aligned16({gu, h, hq, guq})) return misaligned();
     return launch_swiglu(gu, dt, rows, I, h, hq, h_scale, guq, gu_scale, static_cast<hipStream_t>(stream));
 }
@@ -605,6 +633,7 @@ moe_status moe_swiglu_backward(const void* dh, int dt, const uint8_t* guq, const
     if (rows == 0) return MOE_OK;
     if (!dh || !guq || !gu_scale || !d_gu)
         return set_error(MOE_ERR_INVALID_ARG, "dh, guq, gu_scale and d_gu must be non-null");
+    if (is_any(d_gu, {dh, guq, gu_scale, h}) || is_any(h, {guq, gu_scale})) return same_buffer();
     if (!aligned16({dh, guq, d_gu, h})) return misaligned();
     return launch_swiglu_backward(dh, dt, guq, gu_scale, rows, I, d_gu, h, static_cast<hipStream_t>(stream));
 }

@@ -526,6 +526,49 @@ def test_swiglu_saturated_gates():
         assert bool(d.isfinite().all())
 
 
+# ------------------------------------------------------------------ alignment
+def shifted(t):
+    """The same values at an address that is one element past a 16-byte boundary."""
+    buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)
+    buf[1:] = t.reshape(-1).to(DEV)
+    return buf[1:].view(t.shape)
+
+
+def test_elements_alone_aligned():
+    """Scales, ids, places and logits need only their element's alignment."""
+    T, H, E, k, I = 37, 256, 16, 3, 128
+    up = spread(T, E, k)
+    x, w, l, sc = rnd(T, H).to(DEV), torch.ones(H, device=DEV), rnd(T, E), rnd(T, k, seed=1)
+    ids = l.topk(k, 1).indices.int()
+    ys = shifted(torch.zeros(T, H // 128))
+    want = moe.rmsnorm(x, w, quantize=True)
+    got = moe.rmsnorm(x, w, quantize=True, out=(None, None, None, ys))
+    assert got[3].data_ptr() % 16 == 4
+    same(got[3], want[3], "y_scale")
+    rs = shifted(torch.zeros(T * k, H // 128))
+    a, b = moe.dispatch(want[2], shifted(up), k, x_scale=shifted(want[3].cpu()), out=(None, rs)), \
+        moe.dispatch(want[2], up.to(DEV), k, x_scale=want[3])
+    same(a[0], b[0], "rows")
+    same(a[1], b[1], "rows_scale")
+    rows = moe.dispatch(x, up.to(DEV), k)
+    same(moe.dispatch_backward(rows, shifted(up), k), moe.dispatch_backward(rows, up.to(DEV), k), "dx")
+    a = moe.finalize_backward(x, rows, shifted(up), shifted(sc), out=(None, shifted(torch.zeros(T, k))))
+    b = moe.finalize_backward(x, rows, up.to(DEV), sc.to(DEV))
+    same(a[0], b[0], "d_fc2")
+    same(a[1], b[1], "d_scales")
+    for method in range(7):
+        same(moe.route_backward(shifted(l), shifted(ids), shifted(sc), method),
+             moe.route_backward(l.to(DEV), ids.to(DEV), sc.to(DEV), method), f"d_logits, method {method}")
+    gu = rnd(T, 2 * I, seed=3).to(DEV)
+    want = moe.swiglu(gu, quantize=True, checkpoint=True, want_h=True)
+    got = moe.swiglu(gu, quantize=True, checkpoint=True, want_h=True,
+                     out=(None, None, shifted(torch.zeros(T, 1)), None, shifted(torch.zeros(T, 2))))
+    same(got[2], want[2], "h_scale")
+    same(got[4], want[4], "gu_scale")
+    same(moe.swiglu_backward(want[0], want[3], shifted(want[4].cpu()))[0],
+         moe.swiglu_backward(want[0], want[3], want[4])[0], "d_gu")
+
+
 # ------------------------------------------------------- empty calls, refusals
 def test_no_rows():
     w = torch.ones(256, device=DEV)

@@ -2,6 +2,8 @@
 the host checks of every entry point (bad arguments are refused before
 anything is launched; the pointers here are never dereferenced)."""
 import ctypes as C
+import os
+import re
 
 import numpy as np
 import pytest
@@ -12,14 +14,13 @@ import rowops_ref as ref
 from mixture_experts_layer_07_amd import binding
 
 OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
-P = C.c_void_p(1 << 20)
 ODD = C.c_void_p((1 << 20) + 4)
+A, B, D, E, F, G, I, J, K = (C.c_void_p(n << 24) for n in range(1, 10))  # buffers, never dereferenced
 F32, BF16, FP8 = 0, 1, 2
 
 
 @pytest.fixture(scope="module")
 def L():
-    import os
     if not os.path.exists(binding.LIB_PATH):
         from mixture_experts_layer_07_amd import build
         build.build(verbose=False)
@@ -82,31 +83,34 @@ def test_swiglu_formula():
 
 # ------------------------------------------------------------------- refusals
 def test_rmsnorm_validation(L):
-    def f(x=P, r=None, w=P, dt=BF16, T=4, H=256, eps=1e-6, total=None, y=P, q=None, s=None):
+    def f(x=A, r=None, w=B, dt=BF16, T=4, H=256, eps=1e-6, total=None, y=D, q=None, s=None):
         return L.moe_rmsnorm(x, r, w, dt, T, H, eps, total, y, q, s, None)
 
-    Q = C.c_void_p(1 << 21)
     assert f(T=-1) == INVALID and f(H=0) == INVALID and f(dt=FP8) == INVALID and f(dt=7) == INVALID
     assert f(H=100) == UNSUPPORTED                          # H % 8
     assert f(H=16392) == UNSUPPORTED and "16384" in binding.last_error()
     assert f(T=(1 << 30) + 1) == UNSUPPORTED
-    assert f(H=264, q=P, s=P) == UNSUPPORTED                # codes need H % 128
+    assert f(H=264, q=E, s=F) == UNSUPPORTED                # codes need H % 128
     for eps in (0.0, -1e-6, float("inf"), float("nan")):
         assert f(eps=eps) == INVALID
     assert f(x=None) == INVALID and f(w=None) == INVALID
-    assert f(r=P) == INVALID and f(total=P) == INVALID      # residual and total together
-    assert f(q=P) == INVALID and f(s=P) == INVALID          # codes and scales together
+    assert f(r=E) == INVALID and f(total=E) == INVALID      # residual and total together
+    assert f(q=E) == INVALID and f(s=E) == INVALID          # codes and scales together
     assert f(y=None) == INVALID                             # nothing to write
-    assert f(r=P, total=Q, y=Q) == INVALID                  # two outputs, one buffer
+    full = dict(x=A, r=E, w=B, total=F, y=D, q=G, s=I)
+    for out, others in (("y", ("total", "r", "w", "q", "s")), ("total", ("w", "q", "s")), ("q", ("x", "r", "w", "s")),
+                        ("s", ("x", "r", "w"))):
+        for other in others:
+            assert f(**{**full, out: full[other]}) == INVALID and "same buffer" in binding.last_error()
     for name in ("x", "r", "w", "total", "y", "q"):
-        a = dict(x=P, r=P, w=P, total=Q, y=P, q=P, s=P)
+        a = dict(full)
         a[name] = ODD
         assert f(**a) == INVALID and "aligned" in binding.last_error()
     assert f(x=None, w=None, y=None, T=0) == OK
 
 
 def test_rmsnorm_backward_validation(L):
-    def f(dy=P, z=P, w=P, d=None, dt=BF16, T=4, H=256, eps=1e-6, dz=P, dw=P, ws=P, n=1 << 30):
+    def f(dy=A, z=B, w=D, d=None, dt=BF16, T=4, H=256, eps=1e-6, dz=E, dw=F, ws=G, n=1 << 30):
         return L.moe_rmsnorm_backward(dy, z, w, d, dt, T, H, eps, dz, dw, ws, n, None)
 
     assert f(T=-1) == INVALID and f(H=0) == INVALID and f(dt=FP8) == INVALID and f(eps=0.0) == INVALID
@@ -115,6 +119,8 @@ def test_rmsnorm_backward_validation(L):
         assert f(**{name: None}) == INVALID
     for name in ("dy", "z", "w", "d", "dz", "ws"):
         assert f(**{name: ODD}) == INVALID
+    for name, value in (("dz", B), ("dz", D), ("dz", F), ("dz", G), ("dw", A), ("dw", B), ("dw", G), ("ws", A), ("ws", D)):
+        assert f(**{name: value}) == INVALID and "same buffer" in binding.last_error()
     assert f(ws=None) == WORKSPACE
     need = L.moe_rmsnorm_backward_workspace_size(4, 256)
     assert need > 0 and f(n=need - 1) == WORKSPACE
@@ -125,29 +131,31 @@ def test_rmsnorm_backward_validation(L):
 
 
 def test_dispatch_validation(L):
-    def f(x=P, xs=None, dt=BF16, T=4, H=256, k=2, sh=0, up=P, rows=P, rs=None):
+    def f(x=A, xs=None, dt=BF16, T=4, H=256, k=2, sh=0, up=B, rows=D, rs=None):
         return L.moe_dispatch(x, xs, dt, T, H, k, sh, up, rows, rs, None)
 
     assert f(T=-1) == INVALID and f(k=0) == INVALID and f(sh=-1) == INVALID and f(sh=65) == INVALID
     assert f(k=9) == UNSUPPORTED and f(H=100) == UNSUPPORTED and f(dt=5) == INVALID and f(H=0) == INVALID
-    assert f(dt=FP8, H=264, xs=P, rs=P) == UNSUPPORTED
-    assert f(dt=FP8) == INVALID and f(dt=FP8, xs=P) == INVALID and f(xs=P, rs=P) == INVALID
+    assert f(dt=FP8, H=264, xs=E, rs=F) == UNSUPPORTED
+    assert f(dt=FP8) == INVALID and f(dt=FP8, xs=E) == INVALID and f(xs=E, rs=F) == INVALID
+    assert f(rows=A) == INVALID and f(rows=B) == INVALID and f(dt=FP8, xs=E, rs=E) == INVALID
+    assert f(dt=FP8, xs=E, rs=A) == INVALID and f(dt=FP8, xs=E, rs=D) == INVALID
     assert f(x=None) == INVALID and f(up=None) == INVALID and f(rows=None) == INVALID
     assert f(x=ODD) == INVALID and f(rows=ODD) == INVALID
     assert f(T=1 << 29, k=4) == UNSUPPORTED and f(H=(1 << 28) + 8) == UNSUPPORTED
     assert f(T=0, x=None, up=None, rows=None) == OK
 
-    def g(d=P, dt=BF16, up=P, T=4, k=2, H=256, sh=0, dx=P, dxt=BF16):
+    def g(d=A, dt=BF16, up=B, T=4, k=2, H=256, sh=0, dx=D, dxt=BF16):
         return L.moe_dispatch_backward(d, dt, up, T, k, H, sh, dx, dxt, None)
 
     assert g(dt=FP8) == INVALID and g(dxt=FP8) == INVALID and g(k=9) == UNSUPPORTED and g(H=4) == UNSUPPORTED
     assert g(d=None) == INVALID and g(up=None) == INVALID and g(dx=None) == INVALID
-    assert g(d=ODD) == INVALID and g(dx=ODD) == INVALID
+    assert g(d=ODD) == INVALID and g(dx=ODD) == INVALID and g(dx=A) == INVALID
     assert g(T=0, d=None, up=None, dx=None) == OK
 
 
 def test_finalize_backward_validation(L):
-    def f(dy=P, dyt=BF16, r=P, dt=BF16, up=P, sc=P, T=4, k=2, H=256, sh=0, d=P, ds=P):
+    def f(dy=A, dyt=BF16, r=B, dt=BF16, up=D, sc=E, T=4, k=2, H=256, sh=0, d=F, ds=G):
         return L.moe_finalize_backward(dy, dyt, r, dt, up, sc, T, k, H, sh, d, ds, None)
 
     assert f(T=-1) == INVALID and f(dyt=FP8) == INVALID and f(dt=FP8) == INVALID
@@ -156,11 +164,13 @@ def test_finalize_backward_validation(L):
         assert f(**{name: None}) == INVALID
     for name in ("dy", "r", "d"):
         assert f(**{name: ODD}) == INVALID
+    for name, value in (("d", A), ("d", E), ("ds", A), ("ds", B), ("ds", E), ("ds", F)):
+        assert f(**{name: value}) == INVALID and "same buffer" in binding.last_error()
     assert f(T=0, dy=None, r=None, up=None, sc=None, d=None, ds=None) == OK
 
 
 def test_route_backward_validation(L):
-    def f(l=P, i=P, d=P, T=4, E=16, method=0, k=2, sc=1.0, flags=0, out=P):
+    def f(l=A, i=B, d=D, T=4, E=16, method=0, k=2, sc=1.0, flags=0, out=F):
         return L.moe_route_backward(l, i, d, T, E, method, k, sc, flags, out, None)
 
     assert f(T=-1) == INVALID and f(k=0) == INVALID and f(k=17) == INVALID and f(E=0) == INVALID
@@ -170,24 +180,29 @@ def test_route_backward_validation(L):
     assert f(sc=float("nan")) == INVALID
     for name in ("l", "i", "d", "out"):
         assert f(**{name: None}) == INVALID
-    assert f(out=ODD) == INVALID
+    assert f(out=ODD) == INVALID and f(out=A) == INVALID and f(out=D) == INVALID
     assert f(T=0, l=None, i=None, d=None, out=None) == OK
 
 
 def test_swiglu_validation(L):
-    def f(gu=P, dt=BF16, rows=4, I=256, h=P, hq=None, hs=None, q=None, qs=None):
+    def f(gu=A, dt=BF16, rows=4, I=256, h=B, hq=None, hs=None, q=None, qs=None):
         return L.moe_swiglu(gu, dt, rows, I, h, hq, hs, q, qs, None)
 
     assert f(rows=-1) == INVALID and f(I=0) == INVALID and f(dt=FP8) == INVALID and f(gu=None) == INVALID
-    assert f(I=12) == UNSUPPORTED and f(I=264, q=P, qs=P) == UNSUPPORTED and f(I=264, hq=P, hs=P) == UNSUPPORTED
+    assert f(I=12) == UNSUPPORTED and f(I=264, q=F, qs=G) == UNSUPPORTED and f(I=264, hq=D, hs=E) == UNSUPPORTED
     assert f(rows=(1 << 30) + 1) == UNSUPPORTED and f(I=(1 << 29) + 128) == UNSUPPORTED
     assert f(h=None) == INVALID
-    assert f(hq=P) == INVALID and f(hs=P) == INVALID and f(q=P) == INVALID and f(qs=P) == INVALID
+    assert f(hq=D) == INVALID and f(hs=E) == INVALID and f(q=F) == INVALID and f(qs=G) == INVALID
     assert f(gu=ODD) == INVALID and f(h=ODD) == INVALID
-    assert f(hq=ODD, hs=P) == INVALID and f(q=ODD, qs=P) == INVALID
+    assert f(hq=ODD, hs=E) == INVALID and f(q=ODD, qs=G) == INVALID
+    full = dict(gu=A, h=B, hq=D, hs=E, q=F, qs=G)
+    for a in full:
+        for b in full:
+            if a != b:
+                assert f(**{**full, a: full[b]}) == INVALID and "same buffer" in binding.last_error()
     assert f(rows=0, gu=None, h=None) == OK
 
-    def g(dh=P, dt=BF16, q=P, qs=P, rows=4, I=256, d=P, h=None):
+    def g(dh=A, dt=BF16, q=B, qs=D, rows=4, I=256, d=E, h=None):
         return L.moe_swiglu_backward(dh, dt, q, qs, rows, I, d, h, None)
 
     assert g(rows=-1) == INVALID and g(I=0) == INVALID and g(dt=FP8) == INVALID
@@ -196,6 +211,8 @@ def test_swiglu_validation(L):
         assert g(**{name: None}) == INVALID
     for name in ("dh", "q", "d", "h"):
         assert g(**{name: ODD}) == INVALID
+    for name, value in (("d", A), ("d", B), ("d", D), ("h", B), ("h", E)):
+        assert g(**{name: value}) == INVALID and "same buffer" in binding.last_error()
     assert g(rows=0, dh=None, q=None, qs=None, d=None) == OK
 
 
@@ -230,8 +247,8 @@ def test_call_checks_its_arguments(L):
 
 def test_call_covers_every_kernel_entry():
     """Each entry point that launches is known to the native half (it asks for its arguments)."""
-    import re
-    text = open(__file__.replace("tests/test_rowops_abi.py", "include/moe.h")).read()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    text = open(os.path.join(root, "include", "moe.h")).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     launching = re.findall(r"moe_status (moe_\w+)\([^;]*void\* stream\);", text)
     assert len(launching) >= 17
