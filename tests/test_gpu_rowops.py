@@ -344,7 +344,7 @@ def test_dropped_pairs(dt):
 
 
 # -------------------------------------------------------------- routing weights
-ROUTES = [(1, 8, 1), (1, 256, 8), (31, 7, 7), (33, 65, 3), (100, 256, 8), (64, 12, 2), (1029, 9, 4), (70, 255, 5)]
+ROUTES = [(1, 1, 1), (11, 2, 2), (1, 8, 1), (1, 256, 8), (31, 7, 7), (33, 65, 3), (100, 256, 8), (64, 12, 2), (1029, 9, 4), (70, 255, 5)]
 
 
 @pytest.mark.parametrize("method,renorm", [(0, False), (0, True), (1, False), (2, False), (3, False), (4, False),

@@ -124,6 +124,42 @@ def test_swiglu(rows, I):
             same(m[a:b], n, f"{what} of rows {a} to {b}")
 
 
+@pytest.mark.parametrize("dt", [BF, FP])
+def test_in_place_past_the_caches(dt):
+    """The in-place forms at sizes that stream past the caches: the same bits as with buffers apart."""
+    T, H = (4000, 7168) if dt == BF else (2000, 7168)
+    x, r, w = rnd(T, H, dt=dt), rnd(T, H, seed=1, dt=dt), rnd(1, H, seed=2, dt=dt)[0]
+    want = moe.rmsnorm(x, w, residual=r, quantize=True)
+    for into in (0, 1):
+        a = [x.clone(), r.clone()]
+        got = moe.rmsnorm(a[0], w, residual=a[1], quantize=True, out=(None, a[into], None, None))
+        for m, n, what in zip(got, want, ("y", "total", "codes", "scales")):
+            same(m, n, f"{what}, total in place {into}")
+    want = moe.rmsnorm_backward(r, x, w, dsum=r)
+    a = r.clone()
+    got = moe.rmsnorm_backward(a, x, w, dsum=r, out=(a, None))
+    same(got[0], want[0], "dz in dy")
+    same(got[1], want[1], "dweight, dz in dy")
+    sh = 1
+    for width in (3, 6):  # both workgroup widths
+        t = T // (width + sh)
+        up = torch.randperm(t * width, generator=torch.Generator(device=DEV).manual_seed(1), device=DEV).int()
+        sc, rows = rnd(t, width, seed=3, dt=FP), x[:t * (width + sh)]
+        want = moe.finalize_backward(r[:t], rows, up, sc, sh)
+        a = rows.clone()
+        got = moe.finalize_backward(r[:t], a, up, sc, sh, out=(a, None))
+        same(got[0], want[0], f"d_fc2 in fc2, k = {width}")
+        same(got[1], want[1], f"d_scales, k = {width}")
+    I = H // 2 // 128 * 128
+    q, s = moe.quantize_fp8(torch.cat([x[:, :I], r[:, :I]], 1).contiguous())
+    dh = x[:, :I].contiguous()
+    want = moe.swiglu_backward(dh, q, s, want_h=True)
+    a = dh.clone()
+    got = moe.swiglu_backward(a, q, s, want_h=True, out=(None, a))
+    same(got[0], want[0], "d_gu, h in dh")
+    same(got[1], want[1], "h in dh")
+
+
 def test_two_threads():
     """Two threads on streams of their own: every result is the one the call gives alone."""
     T, H = 257, 1024
