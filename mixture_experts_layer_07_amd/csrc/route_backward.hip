@@ -115,17 +115,21 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const float* _
             d = 0.0;
         }
         if (!WHOLE && e >= 0) l = logits[t * E + e];
-        // does a token list an expert twice?  (moe_route's ids do not)
+        // does a token list an expert twice?  (moe_route's ids do not.)  Every lane takes part in every
+        // shuffle: a lane that is masked off has nothing to read
         bool again = false;
 #pragma unroll
-        for (int i = 0; i < MOE_MAX_TOPK; ++i) again |= i != j && e >= 0 && __shfl(e, first_lane | i, 64) == e;
+        for (int i = 0; i < MOE_MAX_TOPK; ++i) {
+            const int other = __shfl(e, first_lane | i, 64);
+            again |= i != j && e >= 0 && other == e;
+        }
         const bool twice = __any(again);
         __syncthreads();
         double rest = 0.0;  // what S holds besides the kept weights
         float top = 0.0f;   // maximum logit
         if constexpr (WHOLE) {
             if (twice) {  // every expert once: the first of its pairs takes the others' gradients
-                double sum = 0.0;
+                double sum = -0.0;  // a pair alone keeps its bits, the sign of a zero too
                 bool first = true;
                 for (int i = 0; i < MOE_MAX_TOPK; ++i) {
                     const int ei = __shfl(e, first_lane | i, 64);
@@ -185,7 +189,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(const float* _
             }
             __syncthreads();
         } else if (twice) {  // both lanes write the sum
-            double both = 0.0;
+            double both = -0.0;
             for (int i = 0; i < MOE_MAX_TOPK; ++i) {
                 const int ei = __shfl(e, first_lane | i, 64);
                 const double vi = __shfl(v, first_lane | i, 64);
