@@ -338,6 +338,9 @@ moe_status moe_expert_ffn_fp8_fused(const uint8_t* xq, const float* x_scale, int
  *    call says so (the same pointer is refused, a partial overlap is not seen).
  *  - Rows are independent: a NaN or infinity in one row changes no other row
  *    (dweight, which sums over the rows, excepted).
+ *  - 8-bit outputs: a block of 128 values that holds a NaN has scale NaN, one
+ *    that holds an infinity has scale infinity, so that code * scale is finite
+ *    nowhere in it.  (moe_quantize_fp8 leaves NaN out of a block's maximum.)
  */
 
 /* Widest row of moe_rmsnorm and moe_rmsnorm_backward (a row is held in one
@@ -367,6 +370,8 @@ moe_status moe_expert_ffn_fp8_fused(const uint8_t* xq, const float* x_scale, int
  *  yq, y_scale  device uint8 [T, H] and fp32 [T, H/128] out, both or neither:
  *            the fp32 y (not its `dt` rounding) quantised as moe_quantize_fp8
  *            does.  At least one of y and yq is given.
+ * A NaN in a row makes all of its y NaN, and every block of its codes; an
+ * infinity makes y NaN where it stands (and its block) and 0 elsewhere.
  */
 moe_status moe_rmsnorm(const void* x, const void* residual, const void* weight, int dt, int T, int H,
                        float eps, void* total, void* y, uint8_t* yq, float* y_scale, void* stream);
@@ -493,7 +498,7 @@ moe_status moe_route_backward(const float* logits, const int32_t* ids, const flo
  *  hq, h_scale  device uint8 [rows, I], fp32 [rows, I/128] out, both or
  *            neither: the fp32 h quantised.  At least one of h and hq is given.
  *  guq, gu_scale  device uint8 [rows, 2I], fp32 [rows, 2I/128] out, both or
- *            neither: moe_quantize_fp8 of gu, bit for bit.
+ *            neither: moe_quantize_fp8 of gu, bit for bit where gu holds no NaN.
  */
 moe_status moe_swiglu(const void* gu, int dt, int rows, int I, void* h, uint8_t* hq, float* h_scale,
                       uint8_t* guq, float* gu_scale, void* stream);

@@ -81,12 +81,15 @@ __device__ __forceinline__ float sum16(float v)
     return v;
 }
 
+// Maximum, NaN if either is (fmaxf would drop it): one v_maximum3_f32.
+__device__ __forceinline__ float max_nan(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 __device__ __forceinline__ float max16(float v)
 {
-    v = fmaxf(v, dpp_f32<0xb1>(v));
-    v = fmaxf(v, dpp_f32<0x4e>(v));
-    v = fmaxf(v, dpp_f32<0x141>(v));
-    v = fmaxf(v, dpp_f32<0x140>(v));
+    v = max_nan(v, dpp_f32<0xb1>(v));
+    v = max_nan(v, dpp_f32<0x4e>(v));
+    v = max_nan(v, dpp_f32<0x141>(v));
+    v = max_nan(v, dpp_f32<0x140>(v));
     return v;
 }
 
@@ -99,14 +102,17 @@ __device__ __forceinline__ float wave_sum_f32(float v)
 }
 
 // Maximum of |v| over a 1x128 block, V values a lane: 128 / V consecutive lanes.
+// NaN if the block holds one: its scale is then NaN and no code of it stands for
+// a finite value (a block of NaN alone would otherwise have scale 0 and pass for
+// zeros).
 template <int V>
 __device__ __forceinline__ float block_absmax(const float (&v)[V])
 {
     float m = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(v[i]));
+    for (int i = 0; i < V; ++i) m = max_nan(m, fabsf(v[i]));
     m = max16(m);
-    if constexpr (V == 4) m = fmaxf(m, __shfl_xor(m, 16, 64));
+    if constexpr (V == 4) m = max_nan(m, __shfl_xor(m, 16, 64));
     return m;
 }
 
@@ -128,7 +134,8 @@ __device__ __forceinline__ float quotient(float v, float s, float r)
 // reciprocal a block instead of a division a value, where no residual can
 // underflow (s >= 2^-60: a value that does not round to zero has |v| >= 2^-70,
 // so its residual is a multiple of 2^-118) and nothing overflows; the quotient
-// is then at most 448 (1 + 2^-23), which needs no clamp.  swiglu with a
+// is then at most 448 (1 + 2^-23), which needs no clamp.  A scale that is
+// infinite or NaN takes the other branch.  swiglu with a
 // checkpoint of 73728 x 2048: 210 -> 191 us against a division a value.
 template <int V>
 __device__ __forceinline__ void store_codes(const float (&v)[V], float s, uint8_t* q)
