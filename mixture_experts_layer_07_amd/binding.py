@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import threading
 
 import torch
 
@@ -32,6 +33,7 @@ NOALLOC_SCRATCH_BYTES = 64 << 20
 _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3}
 _lib = None
 _marshal = None
+_loading = threading.Lock()
 
 
 class MoeError(RuntimeError):
@@ -42,52 +44,59 @@ class MoeError(RuntimeError):
 
 def lib():
     """The loaded libmoe.so with argument types set (raises if not built)."""
-    global _lib, _marshal, _dev
     if _lib is None:
-        for path in (LIB_PATH, MARSHAL_PATH):
-            if not os.path.exists(path):
-                raise RuntimeError(f"{path} is not built; run "
-                                   "`python -m mixture_experts_layer_07_amd.build`")
-        L = C.CDLL(LIB_PATH)
-        P, i, u, f, z = C.c_void_p, C.c_int, C.c_uint, C.c_float, C.c_size_t
-        L.moe_route.argtypes = [P, i, i, i, i, i, i, P, f, u, P, P, P]
-        L.moe_permute.argtypes = [P, i, i, i, i, P, P, P, P, z, P]
-        L.moe_expert_ffn.argtypes = [P, i, i, i, i, i, i, i, P, P, P, P, i, P, P, P, P, z, P]
-        L.moe_finalize.argtypes = [P, i, P, P, i, i, i, i, P, i, P]
-        L.moe_quantize_fp8.argtypes = [P, i, i, i, P, P, P]
-        L.moe_expert_ffn_fp8.argtypes = [P, P, i, i, i, i, i, i, P, P, P, P, P, P, P, P, z, P]
-        L.moe_expert_ffn_noalloc.argtypes = [P, i, i, i, i, i, i, i, P, P, P, P, i, P, P, P, P]
-        L.moe_expert_ffn_fused.argtypes = [P, i, i, i, i, i, i, i, P, P, P, P, i, P, P, i, P, P]
-        L.moe_expert_ffn_fp8_fused.argtypes = [P, P, i, i, i, i, i, i, P, P, P, P, P, P, i, P, P]
-        L.moe_rmsnorm.argtypes = [P, P, P, i, i, i, f, P, P, P, P, P]
-        L.moe_rmsnorm_backward.argtypes = [P, P, P, P, i, i, i, f, P, P, P, z, P]
-        L.moe_rmsnorm_backward_workspace_size.argtypes = [i, i]
-        L.moe_rmsnorm_backward_workspace_size.restype = z
-        L.moe_dispatch.argtypes = [P, P, i, i, i, i, i, P, P, P, P]
-        L.moe_dispatch_backward.argtypes = [P, i, P, i, i, i, i, P, i, P]
-        L.moe_finalize_backward.argtypes = [P, i, P, i, P, P, i, i, i, i, P, P, P]
-        L.moe_route_backward.argtypes = [P, P, P, i, i, i, i, f, u, P, P]
-        L.moe_swiglu.argtypes = [P, i, i, i, P, P, P, P, P, P]
-        L.moe_swiglu_backward.argtypes = [P, i, P, P, i, i, P, P, P]
-        L.moe_workspace_size.argtypes = [i, i, i, i, i, i, i]
-        L.moe_workspace_size.restype = z
-        L.moe_status_string.argtypes = [i]
-        L.moe_status_string.restype = C.c_char_p
-        L.moe_last_error.argtypes = []
-        L.moe_last_error.restype = C.c_char_p
-        L.moe_timing_enable.argtypes = [i]
-        L.moe_kernel_times.argtypes = [P, P, i]
-        for fn in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_expert_ffn_noalloc", "moe_finalize",
-                   "moe_quantize_fp8", "moe_expert_ffn_fp8", "moe_expert_ffn_fused",
-                   "moe_expert_ffn_fp8_fused", "moe_rmsnorm", "moe_rmsnorm_backward",
-                   "moe_dispatch", "moe_dispatch_backward", "moe_finalize_backward",
-                   "moe_route_backward", "moe_swiglu", "moe_swiglu_backward",
-                   "moe_timing_enable", "moe_kernel_times"):
-            getattr(L, fn).restype = C.c_int
-        from . import _marshal as native
-        native.setup(lambda fn: C.cast(getattr(L, fn), C.c_void_p).value, _failed, _refuse)
-        _lib, _marshal, _dev = L, native, native.check
+        with _loading:  # threads that make their first call together load once
+            if _lib is None:
+                _load()
     return _lib
+
+
+def _load():
+    global _lib, _marshal, _dev
+    for path in (LIB_PATH, MARSHAL_PATH):
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is not built; run "
+                               "`python -m mixture_experts_layer_07_amd.build`")
+    L = C.CDLL(LIB_PATH)
+    P, i, u, f, z = C.c_void_p, C.c_int, C.c_uint, C.c_float, C.c_size_t
+    L.moe_route.argtypes = [P, i, i, i, i, i, i, P, f, u, P, P, P]
+    L.moe_permute.argtypes = [P, i, i, i, i, P, P, P, P, z, P]
+    L.moe_expert_ffn.argtypes = [P, i, i, i, i, i, i, i, P, P, P, P, i, P, P, P, P, z, P]
+    L.moe_finalize.argtypes = [P, i, P, P, i, i, i, i, P, i, P]
+    L.moe_quantize_fp8.argtypes = [P, i, i, i, P, P, P]
+    L.moe_expert_ffn_fp8.argtypes = [P, P, i, i, i, i, i, i, P, P, P, P, P, P, P, P, z, P]
+    L.moe_expert_ffn_noalloc.argtypes = [P, i, i, i, i, i, i, i, P, P, P, P, i, P, P, P, P]
+    L.moe_expert_ffn_fused.argtypes = [P, i, i, i, i, i, i, i, P, P, P, P, i, P, P, i, P, P]
+    L.moe_expert_ffn_fp8_fused.argtypes = [P, P, i, i, i, i, i, i, P, P, P, P, P, P, i, P, P]
+    L.moe_rmsnorm.argtypes = [P, P, P, i, i, i, f, P, P, P, P, P]
+    L.moe_rmsnorm_backward.argtypes = [P, P, P, P, i, i, i, f, P, P, P, z, P]
+    L.moe_rmsnorm_backward_workspace_size.argtypes = [i, i]
+    L.moe_rmsnorm_backward_workspace_size.restype = z
+    L.moe_dispatch.argtypes = [P, P, i, i, i, i, i, P, P, P, P]
+    L.moe_dispatch_backward.argtypes = [P, i, P, i, i, i, i, P, i, P]
+    L.moe_finalize_backward.argtypes = [P, i, P, i, P, P, i, i, i, i, P, P, P]
+    L.moe_route_backward.argtypes = [P, P, P, i, i, i, i, f, u, P, P]
+    L.moe_swiglu.argtypes = [P, i, i, i, P, P, P, P, P, P]
+    L.moe_swiglu_backward.argtypes = [P, i, P, P, i, i, P, P, P]
+    L.moe_workspace_size.argtypes = [i, i, i, i, i, i, i]
+    L.moe_workspace_size.restype = z
+    L.moe_status_string.argtypes = [i]
+    L.moe_status_string.restype = C.c_char_p
+    L.moe_last_error.argtypes = []
+    L.moe_last_error.restype = C.c_char_p
+    L.moe_timing_enable.argtypes = [i]
+    L.moe_kernel_times.argtypes = [P, P, i]
+    for fn in ("moe_route", "moe_permute", "moe_expert_ffn", "moe_expert_ffn_noalloc", "moe_finalize",
+               "moe_quantize_fp8", "moe_expert_ffn_fp8", "moe_expert_ffn_fused",
+               "moe_expert_ffn_fp8_fused", "moe_rmsnorm", "moe_rmsnorm_backward",
+               "moe_dispatch", "moe_dispatch_backward", "moe_finalize_backward",
+               "moe_route_backward", "moe_swiglu", "moe_swiglu_backward",
+               "moe_timing_enable", "moe_kernel_times"):
+        getattr(L, fn).restype = C.c_int
+    from . import _marshal as native
+    native.setup(lambda fn: C.cast(getattr(L, fn), C.c_void_p).value, _failed, _refuse)
+    _marshal, _dev = native, native.check
+    _lib = L  # last: where it is set, the rest is
 
 
 def status_string(st: int) -> str:
