@@ -368,6 +368,10 @@ def finalize(fc2_out, unpermute, scales, n_shared=0, out_dtype=None, out=None):
 
 
 # ----------------------------------------------------------- row operators
+# None of them records a graph.  With gradients enabled, rmsnorm, dispatch and swiglu warn
+# (UserWarning) of a tensor that requires grad: their results are constants to autograd.  A training
+# program calls the backward functions itself, for example from a torch.autograd.Function, whose
+# forward and backward run with gradients disabled.
 def _out(t, name, shape, dtype, device):
     """The caller's output buffer `t`, checked, or a new one."""
     if t is None:

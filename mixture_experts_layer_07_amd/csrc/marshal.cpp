@@ -10,6 +10,7 @@
 // binding.py; this module gets the functions' addresses.
 #include <Python.h>
 
+#include <c10/core/GradMode.h>
 #include <torch/csrc/Device.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -36,7 +37,8 @@ PyObject* g_stream = nullptr;
 // ------------------------------------------------------------------- call
 struct Call {
     const char* name;
-    long index;  // device
+    long index;    // device
+    bool forward;  // a row operator that has a backward call of its own
 };
 
 bool convert(PyObject* o, const Call& c, void** out)
@@ -50,6 +52,14 @@ bool convert(PyObject* o, const Call& c, void** out)
         return false;
     }
     const at::Tensor& t = THPVariable_Unpack(o);
+    // A result that autograd takes for a constant must not lose the caller's gradient without a word.
+    // (The gradients' calls may well take such tensors: a caller's own products under autograd.)
+    if (c.forward && t.requires_grad() && c10::GradMode::is_enabled()) {
+        const std::string text = std::string(c.name) +
+                                 ": a tensor requires grad, but the call records no graph; detach it or call under "
+                                 "torch.no_grad(), and use the backward call";
+        if (PyErr_WarnEx(PyExc_UserWarning, text.c_str(), 3)) return false;  // warnings may be errors
+    }
     if (!t.is_cuda() || t.device().index() != c.index) {
         PyErr_Format(PyExc_ValueError, "%s: a tensor on %s, expected cuda:%ld", c.name, t.device().str().c_str(),
                      c.index);
@@ -147,36 +157,37 @@ int run_any(moe_status (*f)(A...), const Call& c, PyObject* const* args, Py_ssiz
 struct Entry {
     const char* name;
     int (*run)(void*, const Call&, PyObject* const*, Py_ssize_t);
+    bool forward;
     void* address;
 };
 
-#define MOE_ENTRY(fn)                                                                                    \
+#define MOE_ENTRY(fn, forward)                                                                               \
     {                                                                                                    \
         #fn,                                                                                             \
             [](void* f, const Call& c, PyObject* const* a, Py_ssize_t n) {                               \
                 return run_any(reinterpret_cast<decltype(&fn)>(f), c, a, n);                             \
             },                                                                                           \
-            nullptr                                                                                      \
+            forward, nullptr                                                                             \
     }
 
 Entry g_entries[] = {
-    MOE_ENTRY(moe_route),
-    MOE_ENTRY(moe_permute),
-    MOE_ENTRY(moe_expert_ffn),
-    MOE_ENTRY(moe_expert_ffn_noalloc),
-    MOE_ENTRY(moe_expert_ffn_fp8),
-    MOE_ENTRY(moe_expert_ffn_fused),
-    MOE_ENTRY(moe_expert_ffn_fp8_fused),
-    MOE_ENTRY(moe_finalize),
-    MOE_ENTRY(moe_quantize_fp8),
-    MOE_ENTRY(moe_rmsnorm),
-    MOE_ENTRY(moe_rmsnorm_backward),
-    MOE_ENTRY(moe_dispatch),
-    MOE_ENTRY(moe_dispatch_backward),
-    MOE_ENTRY(moe_finalize_backward),
-    MOE_ENTRY(moe_route_backward),
-    MOE_ENTRY(moe_swiglu),
-    MOE_ENTRY(moe_swiglu_backward),
+    MOE_ENTRY(moe_route, false),
+    MOE_ENTRY(moe_permute, false),
+    MOE_ENTRY(moe_expert_ffn, false),
+    MOE_ENTRY(moe_expert_ffn_noalloc, false),
+    MOE_ENTRY(moe_expert_ffn_fp8, false),
+    MOE_ENTRY(moe_expert_ffn_fused, false),
+    MOE_ENTRY(moe_expert_ffn_fp8_fused, false),
+    MOE_ENTRY(moe_finalize, false),
+    MOE_ENTRY(moe_quantize_fp8, false),
+    MOE_ENTRY(moe_rmsnorm, true),
+    MOE_ENTRY(moe_rmsnorm_backward, false),
+    MOE_ENTRY(moe_dispatch, true),
+    MOE_ENTRY(moe_dispatch_backward, false),
+    MOE_ENTRY(moe_finalize_backward, false),
+    MOE_ENTRY(moe_route_backward, false),
+    MOE_ENTRY(moe_swiglu, true),
+    MOE_ENTRY(moe_swiglu_backward, false),
 };
 
 // A tensor without storage of its own makes torch throw: no exception leaves
@@ -214,7 +225,8 @@ PyObject* call_(PyObject* const* args, Py_ssize_t n)
         if (PyErr_Occurred()) return nullptr;
         entry->address = reinterpret_cast<void*>(a);
     }
-    const int st = entry->run(entry->address, Call{entry->name, dev.has_index() ? (long)dev.index() : -1}, args + 2, n - 2);
+    const int st = entry->run(entry->address, Call{entry->name, dev.has_index() ? (long)dev.index() : -1, entry->forward},
+                              args + 2, n - 2);
     if (st < 0) return nullptr;
     if (st != MOE_OK) {
         PyObject* r = PyObject_CallFunction(g_failed, "si", name, st);
