@@ -336,6 +336,9 @@ moe_status moe_expert_ffn_fp8_fused(const uint8_t* xq, const float* x_scale, int
  *    alignment.
  *  - An output may not overlap an input or another output except where the
  *    call says so (the same pointer is refused, a partial overlap is not seen).
+ *  - The same inputs give the same bits.  A row's result does not depend on its
+ *    place nor on how many rows there are, but for moe_finalize_backward's
+ *    d_scales, whose order of summation follows the call's size, and dweight.
  *  - Rows are independent: a NaN or infinity in one row changes no other row
  *    (dweight, which sums over the rows, excepted).
  *  - 8-bit outputs: a block of 128 values that holds a NaN has scale NaN, one
@@ -449,7 +452,10 @@ moe_status moe_dispatch_backward(const void* d_rows, int dt, const int32_t* unpe
  *  dy        device [T, H] in `dyt` (MOE_F32 or MOE_BF16).
  *  fc2_out   device [T*k + n_shared*T, H] in `dt`, as given to moe_finalize.
  *  unpermute, scales   as given to moe_finalize.  A dropped pair (entry outside
- *            [0, T*k)) gets d_scales 0, and no row is written for it.
+ *            [0, T*k)) gets d_scales 0, and no row is written for it: rows of
+ *            d_fc2 that no pair names are left as they were.  Two pairs with the
+ *            same entry give unspecified contents of that row, and unspecified
+ *            d_scales where d_fc2 is fc2_out.
  *  d_fc2     device [T*k + n_shared*T, H] in `dt` out; may be fc2_out itself.
  *  d_scales  device fp32 [T, k] out: what moe_route_backward takes.
  *  H         a multiple of 8, at most 2^28.
@@ -544,6 +550,11 @@ const char* moe_last_error(void);
  * every launch is bracketed by two HIP events recorded on the launch stream;
  * moe_kernel_times() waits for the recorded events and returns, per kernel
  * id, the summed milliseconds and the launch count since the last reset.
+ *
+ * Ids keep their numbers, and MOE_NUM_KIDS grows with the library's kernels:
+ * moe_kernel_times writes MOE_NUM_KIDS entries of the header that the LIBRARY was
+ * built with, so build its callers again when the library is (10 entries before
+ * the row operators, 19 with them).
  */
 enum {
     MOE_KID_ROUTE = 0,

@@ -458,7 +458,8 @@ def rmsnorm_backward(dy, z, weight, eps=1e-6, dsum=None, ws=None, out=None):
 
 def dispatch(x, unpermute, k, n_shared=0, x_scale=None, out=None):
     """moe_dispatch -> rows [T*k + n_shared*T, H] in expert order; for e4m3 codes x with their
-    x_scale -> (rows, rows_scale), and `out` is such a pair."""
+    x_scale -> (rows, rows_scale), and `out` is such a pair.  Rows that no pair names (unpermute
+    entries outside [0, T*k) are dropped) are not written: a new tensor holds anything there."""
     T, H = _rows_of(x, "x", (torch.float32, torch.bfloat16, torch.float8_e4m3fn))
     d, fp8 = x.device, x.dtype == torch.float8_e4m3fn
     if _places(unpermute, k) != T:
@@ -491,7 +492,7 @@ def dispatch_backward(d_rows, unpermute, k, n_shared=0, out_dtype=None, out=None
 
 def finalize_backward(dy, fc2_out, unpermute, scales, n_shared=0, out=None):
     """moe_finalize_backward -> (d_fc2 [T*k + n_shared*T, H] in fc2_out's dtype, d_scales fp32 [T, k]).
-    out's d_fc2 may be fc2_out."""
+    out's d_fc2 may be fc2_out.  Rows that no pair names are not written, as in dispatch."""
     _dev(scales, "scales", torch.float32)
     T, k = scales.shape
     R, H = _rows_of(fc2_out, "fc2_out", _ACT)

@@ -7,10 +7,13 @@
 // rows are read and summed.  No atomics: every row belongs to one token.
 //
 // Bound by memory.  Measured on MI355X, 8192 tokens x 7168 bf16, k = 8, one shared
-// expert, skewed routing (1.17 GB a copy): dispatch and its gradient in turn 440
-// us (5.3 TB/s; each alone 187 and 178 us), the gradients of finalize 384 us (2.1
-// GB, 5.5 TB/s; 338 us with rows in token order).  Decode batch of 512 tokens'
-// codes 7.1 us.
+// expert, skewed routing (1.17 GB a copy): dispatch and its gradient in turn 441
+// us (5.3 TB/s; each alone 237 and 211 us, 5.0 and 5.6 TB/s), the gradients of
+// finalize 384 us (2.1 GB, 5.5 TB/s; 357 us with rows in token order).  Decode
+// batch of 512 tokens' codes 7.1 us.
+// Every pair of types, 4096 x 7168, k = 4, rows' type first: the gradient of
+// dispatch bf16/bf16 53 us, bf16/fp32 66, fp32/bf16 96, fp32/fp32 106 (5.3 to 5.5
+// TB/s); the gradients of finalize 105, 120, 198, 212 us (4.9 to 5.0 TB/s).
 #include <algorithm>
 
 #include "rowops.h"

@@ -4,9 +4,11 @@
 //     g = dy w,  dz = c (g - n mean(g n)) (+ dtotal),  dw = sum_t dy n
 //
 // Bound by memory: a row stays in registers between its reduction and its
-// outputs, so every array is read and written once.  A wave or, for longer
-// rows, a workgroup owns a row; a thread holds NV 16-byte chunks of V
-// consecutive values at chunk indices tid, tid + stride, ...
+// outputs, so every array is read and written once.  (The gradients of fp32 rows
+// wider than 8192 hold more than fits: 30 registers of a lane go out to scratch
+// memory and come back.)  A wave or, for longer rows, a workgroup owns a row; a
+// thread holds NV 16-byte chunks of V consecutive values at chunk indices tid,
+// tid + stride, ...
 //
 // Measured on MI355X (8192 x 7168 bf16; a copy moves 5.1 TB/s, 6.5 at best):
 //   forward with residual, y and codes  84 us, 6.3 TB/s.  Two chunks a thread:
@@ -16,7 +18,10 @@
 //     two chunks a thread 85 us, one 104 us; the next row's loads in flight over
 //     the reduction 85-105 us (registers), kept only where a row is a chunk a
 //     lane.
-//   one token 5.0 us a call, the gradients of 63 x 256 fp32 5.2 us: launches.
+//   backward of 2048 x 16384 fp32 with dtotal, which spills  103 us, 5.2 TB/s
+//     (2048 x 8192 fp32 48 us, 5.6 TB/s).
+//   one token 5.0 us a call, the kernel 3.4 in a captured graph; the gradients of
+//   63 x 256 fp32 5.2 us, the kernel 4.9.
 #include <algorithm>
 
 #include "rowops.h"

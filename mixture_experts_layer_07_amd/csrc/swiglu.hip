@@ -9,9 +9,9 @@
 // a step; the stride's whole rows and rest come from the host, so no division
 // is made in the loop.
 //
-// Measured on MI355X, 73728 x 2048 bf16: forward with the checkpoint 191 us (1.22
-// GB, 6.4 TB/s), backward with h again 270 us (1.52 GB, 5.6 TB/s), 460 us for the
-// two; 4096 rows to codes of h 8.9 us.  64, 128, 256 threads a workgroup 457, 460,
+// Measured on MI355X, 73728 x 2048 bf16: forward with the checkpoint 202 us (1.22
+// GB, 6.0 TB/s), backward with h again 253 us (1.52 GB, 6.0 TB/s), 461 us for the
+// two in turn; 4096 rows to codes of h 8.9 us.  64, 128, 256 threads a workgroup 457, 460,
 // 475 us; two or four chunks a thread in flight 470, 494 us; 32 bytes a lane in the
 // backward 590 us (half lines a store).
 #include <algorithm>
