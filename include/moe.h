@@ -87,7 +87,7 @@ typedef enum moe_route_method {
  * sum (the renormalize switch of vLLM's FusedTopKRouter). */
 #define MOE_ROUTE_FLAG_RENORMALIZE 1u
 
-typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype;
+typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2, MOE_MXFP4 = 3 } moe_dtype;
 
 /* Shape limits of the kernels (the expert-count and top-k limits of the fused
  * routing kernel on the TensorRT-LLM page, section "融合算子与回退阈值"; its
@@ -97,6 +97,8 @@ typedef enum moe_dtype { MOE_F32 = 0, MOE_BF16 = 1, MOE_FP8_E4M3 = 2 } moe_dtype
 /* Largest intermediate size of the fused FC1+FC2 kernels (h of a 16-row tile
  * is kept in LDS). */
 #define MOE_FUSED_MAX_I 2048
+/* Most tokens of moe_layer_few. */
+#define MOE_FEW_MAX_T 32
 /* Bytes of the library's static device scratch used by moe_expert_ffn_noalloc
  * (64 MiB per GPU the library runs on, held until the process ends). */
 #define MOE_NOALLOC_SCRATCH_BYTES (64u << 20)
@@ -524,9 +526,111 @@ moe_status moe_swiglu(const void* gu, int dt, int rows, int I, void* h, uint8_t*
 moe_status moe_swiglu_backward(const void* dh, int dt, const uint8_t* guq, const float* gu_scale,
                                int rows, int I, void* d_gu, void* h, void* stream);
 
+/*
+ * Microscaled 4-bit floating point (OCP MXFP4), the weights and activations of
+ * the 4-bit fused backends on the TensorRT-LLM page (section "后端的三种形态与两个
+ * 调度器家族").  A row of values is cut into blocks of 32; a block holds 32 e2m1
+ * codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign) and one scale byte s (E8M0) that
+ * stands for 2^(s - 127), 255 for NaN.  Codes are packed two a byte, the even
+ * column in the low half-byte: a [rows, cols] matrix is codes uint8 [rows,
+ * cols/2] and scales uint8 [rows, cols/32].
+ */
+
+/*
+ * moe_quantize_mxfp4 -- rows to codes and scales, of activations (the
+ * quantise-input step) or weights:
+ *     s = max(floor(log2 amax) - 2 + 127, 0),   code = e2m1(v / 2^(s - 127))
+ * rounded to nearest, ties to the even code, saturating at +-6 (a block's
+ * largest value lies between 4 and 8 scales).  A block of zeros has s = 0; a
+ * block that holds a NaN or an infinity has s = 255, which makes every value of
+ * it NaN whatever its code.
+ *
+ *  x      device [rows, cols] in `dt` (MOE_F32 or MOE_BF16), 16-byte aligned.
+ *  cols   a multiple of 32.
+ *  q, scale   device out, q 16-byte aligned.
+ * Bit-exact and deterministic.
+ */
+moe_status moe_quantize_mxfp4(const void* x, int dt, int rows, int cols, uint8_t* q, uint8_t* scale,
+                              void* stream);
+
+/*
+ * moe_dequantize_mxfp4 -- the values that codes and scales stand for, in `dt`
+ * (MOE_F32 or MOE_BF16): exact, but that a value past the type's range is an
+ * infinity (scales above 251 only).  Arguments as for moe_quantize_mxfp4.
+ */
+moe_status moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int rows, int cols, int dt, void* x,
+                                void* stream);
+
+/*
+ * moe_expert_ffn_mxfp4 -- moe_expert_ffn with 4-bit activations and weights on
+ * the scaled fp4 x fp4 MFMA:
+ *     h_r   = silu(W1_g xq_t) * (W3_g xq_t)
+ *     hq_r  = h_r (fp32) quantised like moe_quantize_mxfp4
+ *     out_r = W2_g hq_r
+ * Products are exact, sums fp32; fc2_out is rounded once.
+ *
+ *  xq, x_scale   moe_quantize_mxfp4 of x [T, H].
+ *  w13, w13_scale   device codes [E + n_shared, 2I, H/2] and scales
+ *             [E + n_shared, 2I, H/32]; rows in moe_expert_ffn's order.
+ *  w2, w2_scale   device codes [E + n_shared, H, I/2], scales [.., H, I/32].
+ *  fc2_out    device bf16 [T*k + n_shared*T, H] out (unweighted FFN rows).
+ *  ws         device workspace of moe_workspace_size(T, k, E, n_shared, H, I,
+ *             MOE_MXFP4) bytes.  On return it holds hq: codes [R, I/2] at byte 0
+ *             (R = T*k + n_shared*T, rows in permuted order) and scales
+ *             [R, I/32] from the next 256-byte boundary.
+ * H and I are multiples of 128; xq, hq and one expert's w13 below 4 GiB.  Codes,
+ * scales, fc2_out and ws are 16-byte aligned, and no output is an input.  A NaN
+ * scale of a token makes its rows NaN and no others; one of a weight makes its
+ * output channel NaN (through h, every channel of the expert's rows).
+ * Other arguments as for moe_expert_ffn.
+ */
+moe_status moe_expert_ffn_mxfp4(const uint8_t* xq, const uint8_t* x_scale, int T, int H, int I, int k, int E,
+                                int n_shared, const int32_t* expert_offsets, const int32_t* permuted_pair,
+                                const uint8_t* w13, const uint8_t* w2, const uint8_t* w13_scale,
+                                const uint8_t* w2_scale, void* fc2_out, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * moe_layer_few -- the whole layer for at most MOE_FEW_MAX_T tokens (a decoding
+ * or speculative step), router logits to output, in two kernels:
+ *     ids, scales = moe_route(logits)
+ *     y_t = sum_j scales[t,j] W2_e (silu(W1_e x_t) * (W3_e x_t)),  e = ids[t,j]
+ *           + the shared experts' rows
+ * Each chosen expert's weights are read once.  ids and scales are moe_route's
+ * bit for bit.  h is rounded to the activations' type as in moe_expert_ffn; FC2's
+ * rows are not rounded but summed in fp32, and y is rounded once, so y is not
+ * bit-identical to that of the separate calls.
+ *
+ *  x         device [T, H] in `act`.
+ *  logits, method, k, n_group, topk_group, bias, scaling, flags   as for moe_route.
+ *  act, wdt  MOE_F32 with MOE_F32 weights, or MOE_BF16 with MOE_BF16,
+ *            MOE_FP8_E4M3 or MOE_MXFP4 weights.
+ *  w13, w2, w13_scale, w2_scale   as for moe_expert_ffn; MXFP4 codes and scales
+ *            as for moe_expert_ffn_mxfp4 (the activations stay bf16).
+ *  n_shared  shared experts E .. E + n_shared - 1.
+ *  ids, scales   device int32, fp32 [T, k] out.
+ *  y         device [T, H] out in `act`.
+ *  ws        device workspace of moe_layer_few_workspace_size(...) bytes; on
+ *            return it holds h [T*k + n_shared*T, I], rows in moe_permute's order.
+ * H and I are multiples of 128, at most 2^20.  x, the weights, their scales, y
+ * and ws are 16-byte aligned; no output is an input or another output.  The same
+ * inputs give the same bits.  ids, scales and h of a token do not depend on the
+ * other tokens; y's order of summation does, unless I is a multiple of 1024.
+ * NaN logits of a token give unspecified values in that token's rows.
+ */
+moe_status moe_layer_few(const void* x, int act, const float* logits, int T, int H, int I, int E, int method,
+                         int k, int n_group, int topk_group, const float* bias, float scaling, unsigned flags,
+                         int n_shared, const void* w13, const void* w2, int wdt, const void* w13_scale,
+                         const void* w2_scale, int32_t* ids, float* scales, void* y, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/* Bytes of workspace that moe_layer_few needs (0 on invalid arguments and for
+ * T == 0).  Host-only. */
+size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int k, int n_shared, int act);
+
 /* Bytes of workspace that moe_permute and moe_expert_ffn need for this shape
  * (0 on invalid arguments).  One buffer of this size serves both calls.
- * act = MOE_FP8_E4M3 sizes it for moe_expert_ffn_fp8.  The size depends only
+ * act = MOE_FP8_E4M3 sizes it for moe_expert_ffn_fp8, MOE_MXFP4 for
+ * moe_expert_ffn_mxfp4.  The size depends only
  * on the shape (T*k rows, never on how tokens are routed), so a caller can
  * allocate it once, up front, and reuse it on every call: the gsyq.cn
  * article's remedy for allocator fragmentation in grouped-GEMM MoE layers
@@ -554,7 +658,8 @@ const char* moe_last_error(void);
  * Ids keep their numbers, and MOE_NUM_KIDS grows with the library's kernels:
  * moe_kernel_times writes MOE_NUM_KIDS entries of the header that the LIBRARY was
  * built with, so build its callers again when the library is (10 entries before
- * the row operators, 19 with them).
+ * the row operators, 19 with them, 23 with the 4-bit operators and the layer for few
+ * tokens).
  */
 enum {
     MOE_KID_ROUTE = 0,
@@ -576,7 +681,11 @@ enum {
     MOE_KID_ROUTE_BWD = 16,
     MOE_KID_SWIGLU = 17,
     MOE_KID_SWIGLU_BWD = 18,
-    MOE_NUM_KIDS = 19
+    MOE_KID_QUANT_MXFP4 = 19,
+    MOE_KID_DEQUANT_MXFP4 = 20,
+    MOE_KID_FEW_FC1 = 21,      /* moe_layer_few: routing, FC1, SwiGLU */
+    MOE_KID_FEW_FC2 = 22,      /* ... and FC2 with the weighted sum */
+    MOE_NUM_KIDS = 23
 };
 moe_status moe_timing_enable(int enable);
 moe_status moe_kernel_times(double* ms /*[MOE_NUM_KIDS]*/, int64_t* launches /*[MOE_NUM_KIDS]*/,

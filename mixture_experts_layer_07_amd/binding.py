@@ -20,17 +20,20 @@ LIB_PATH = os.path.join(HERE, "libmoe.so")
 MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
 
 MOE_OK = 0
-F32, BF16, FP8_E4M3 = 0, 1, 2
+F32, BF16, FP8_E4M3, MXFP4 = 0, 1, 2, 3
 ROUTE_DEFAULT, ROUTE_RENORMALIZE, ROUTE_DEEPSEEKV3, ROUTE_RENORMALIZE_NAIVE = 0, 1, 2, 4
 ROUTE_FLAG_RENORMALIZE = 1
 KERNEL_IDS = ["route", "permute_count", "permute_scan", "permute_scatter", "fc1", "fc2",
               "finalize", "quantize", "ffn_fused", "permute_one", "rmsnorm", "rmsnorm_backward",
               "rmsnorm_dweight", "dispatch", "dispatch_backward", "finalize_backward",
-              "route_backward", "swiglu", "swiglu_backward"]
+              "route_backward", "swiglu", "swiglu_backward", "quantize_mxfp4",
+              "dequantize_mxfp4", "few_fc1", "few_fc2"]
 FUSED_MAX_I = 2048
 NOALLOC_SCRATCH_BYTES = 64 << 20
+FEW_MAX_T = 32
 
-_DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3}
+_DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3,
+       torch.float4_e2m1fn_x2: MXFP4}
 _lib = None
 _marshal = None
 _loading = threading.Lock()
@@ -78,6 +81,12 @@ def _load():
     L.moe_route_backward.argtypes = [P, P, P, i, i, i, i, f, u, P, P]
     L.moe_swiglu.argtypes = [P, i, i, i, P, P, P, P, P, P]
     L.moe_swiglu_backward.argtypes = [P, i, P, P, i, i, P, P, P]
+    L.moe_quantize_mxfp4.argtypes = [P, i, i, i, P, P, P]
+    L.moe_dequantize_mxfp4.argtypes = [P, P, i, i, i, P, P]
+    L.moe_expert_ffn_mxfp4.argtypes = [P, P, i, i, i, i, i, i, P, P, P, P, P, P, P, P, z, P]
+    L.moe_layer_few.argtypes = [P, i, P, i, i, i, i, i, i, i, i, P, f, u, i, P, P, i, P, P, P, P, P, P, z, P]
+    L.moe_layer_few_workspace_size.argtypes = [i, i, i, i, i, i, i]
+    L.moe_layer_few_workspace_size.restype = z
     L.moe_workspace_size.argtypes = [i, i, i, i, i, i, i]
     L.moe_workspace_size.restype = z
     L.moe_status_string.argtypes = [i]
@@ -90,7 +99,8 @@ def _load():
                "moe_quantize_fp8", "moe_expert_ffn_fp8", "moe_expert_ffn_fused",
                "moe_expert_ffn_fp8_fused", "moe_rmsnorm", "moe_rmsnorm_backward",
                "moe_dispatch", "moe_dispatch_backward", "moe_finalize_backward",
-               "moe_route_backward", "moe_swiglu", "moe_swiglu_backward",
+               "moe_route_backward", "moe_swiglu", "moe_swiglu_backward", "moe_quantize_mxfp4",
+               "moe_dequantize_mxfp4", "moe_expert_ffn_mxfp4", "moe_layer_few",
                "moe_timing_enable", "moe_kernel_times"):
         getattr(L, fn).restype = C.c_int
     from . import _marshal as native
@@ -148,7 +158,8 @@ def dtype_code(dt: torch.dtype) -> int:
 
 
 def workspace_size(T, k, E, n_shared, H, I, act_dtype) -> int:
-    """act_dtype torch.float8_e4m3fn sizes the workspace of expert_ffn_fp8."""
+    """act_dtype torch.float8_e4m3fn sizes the workspace of expert_ffn_fp8, torch.float4_e2m1fn_x2
+    that of expert_ffn_mxfp4."""
     return int(lib().moe_workspace_size(T, k, E, n_shared, H, I, _DT[act_dtype]))
 
 
@@ -566,6 +577,107 @@ def swiglu_backward(dh, guq, gu_scale, want_h=False, out=None):
         _unused(("h",), (h,))
     _call("moe_swiglu_backward", d, dh, _DT[dt], guq, gu_scale, rows, I, d_gu, h)
     return d_gu, h
+
+
+# ------------------------------------------------------------------- MXFP4
+# Codes are torch.float4_e2m1fn_x2 [.., cols/2] (two a byte, the even column low) and scales
+# torch.float8_e8m0fnu [.., cols/32]; bytes of a checkpoint become them by .view(dtype).
+_CODES, _SCALES = torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
+
+
+def quantize_mxfp4(x, out=None):
+    """moe_quantize_mxfp4 -> (codes float4_e2m1fn_x2 [rows, cols/2], scale float8_e8m0fnu
+    [rows, cols/32]) of x [rows, cols]; weights [.., N, K] go as x.view(-1, K)."""
+    rows, cols = _rows_of(x, "x", _ACT)
+    q, scale = (None, None) if out is None else out
+    q = _out(q, "codes", (rows, cols // 2), _CODES, x.device)
+    scale = _out(scale, "scale", (rows, cols // 32), _SCALES, x.device)
+    _call("moe_quantize_mxfp4", x.device, x, _DT[x.dtype], rows, cols, q, scale)
+    return q, scale
+
+
+def dequantize_mxfp4(codes, scale, dtype=torch.bfloat16, out=None):
+    """moe_dequantize_mxfp4 -> the values [rows, cols] of quantize_mxfp4's codes and scales."""
+    rows, half = _rows_of(codes, "codes", _CODES)
+    if half % 16:
+        raise ValueError(f"codes must be [rows, cols/2] with cols a multiple of 32 (got {tuple(codes.shape)})")
+    _dev(scale, "scale", _SCALES, (rows, half // 16))
+    if dtype not in _ACT:
+        raise ValueError(f"dtype must be one of {_ACT} (got {dtype})")
+    out = _out(out, "x", (rows, 2 * half), dtype, codes.device)
+    _call("moe_dequantize_mxfp4", codes.device, codes, scale, rows, 2 * half, _DT[dtype], out)
+    return out
+
+
+def expert_ffn_mxfp4(xq, x_scale, expert_offsets, permuted_pair, w13, w2, w13_scale, w2_scale, k, E,
+                     n_shared=0, ws=None, out=None):
+    """moe_expert_ffn_mxfp4 -> fc2_out bf16 [T*k + n_shared*T, H]; w13 [G, 2I, H/2] and w2 [G, H, I/2]
+    codes with scales [G, 2I, H/32] and [G, H, I/32]."""
+    T, half = _rows_of(xq, "xq", _CODES)
+    H, G, d = 2 * half, E + n_shared, xq.device
+    _dev(x_scale, "x_scale", _SCALES, (T, H // 32))
+    _dev(w13, "w13", _CODES)
+    if w13.dim() != 3:
+        raise ValueError(f"w13 must be [G, 2I, H/2] (got {tuple(w13.shape)})")
+    I = w13.shape[1] // 2
+    _dev(w13, "w13", shape=(G, 2 * I, half))
+    _dev(w2, "w2", _CODES, (G, H, I // 2))
+    _dev(w13_scale, "w13_scale", _SCALES, (G, 2 * I, H // 32))
+    _dev(w2_scale, "w2_scale", _SCALES, (G, H, I // 32))
+    _dev(expert_offsets, "expert_offsets", torch.int32, (G + 1,))
+    _dev(permuted_pair, "permuted_pair", torch.int32, (T * k,))
+    R = T * k + n_shared * T
+    out = _out(out, "fc2_out", (R, H), torch.bfloat16, d)
+    if ws is None:
+        ws = alloc_workspace(T, k, E, n_shared, H, I, _CODES, d)
+    _dev(ws, "ws", torch.uint8)
+    _call("moe_expert_ffn_mxfp4", d, xq, x_scale, T, H, I, k, E, n_shared, expert_offsets, permuted_pair,
+          w13, w2, w13_scale, w2_scale, out, ws, ws.numel())
+    return out
+
+
+# ------------------------------------------------------------ a few tokens
+def layer_few_workspace(T, H, I, E, k, n_shared=0, act_dtype=torch.bfloat16, device="cuda") -> torch.Tensor:
+    n = int(lib().moe_layer_few_workspace_size(T, H, I, E, k, n_shared, _DT[act_dtype]))
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def layer_few(x, logits, w13, w2, k, method, w13_scale=None, w2_scale=None, n_group=1, topk_group=1, bias=None,
+              scaling=1.0, renormalize=False, n_shared=0, ws=None, out=None):
+    """moe_layer_few, the whole layer for at most FEW_MAX_T tokens -> (y [T, H] in x's dtype, ids int32
+    [T, k], scales fp32 [T, k]).  Weights as expert_ffn takes them, or as expert_ffn_mxfp4 does (by
+    w13's dtype); `out` is the same tuple of buffers."""
+    T, H = _rows_of(x, "x", _ACT)
+    d = x.device
+    if _rows_of(logits, "logits", torch.float32)[0] != T:
+        raise ValueError(f"logits has {logits.shape[0]} rows, expected {T}")
+    E = logits.shape[1]
+    G = E + n_shared
+    if bias is not None:
+        _dev(bias, "bias", torch.float32, (E,))
+    _dev(w13, "w13", (torch.float32, torch.bfloat16, torch.float8_e4m3fn, _CODES))
+    if w13.dim() != 3:
+        raise ValueError(f"w13 must be [G, 2I, H] (got {tuple(w13.shape)})")
+    I, mx = w13.shape[1] // 2, w13.dtype == _CODES
+    _dev(w13, "w13", shape=(G, 2 * I, H // 2 if mx else H))
+    _dev(w2, "w2", w13.dtype, (G, H, I // 2 if mx else I))
+    if mx:
+        _dev(w13_scale, "w13_scale", _SCALES, (G, 2 * I, H // 32))
+        _dev(w2_scale, "w2_scale", _SCALES, (G, H, I // 32))
+    elif w13.dtype == torch.float8_e4m3fn:
+        _dev(w13_scale, "w13_scale", torch.float32, (G, 2 * I // 128, H // 128))
+        _dev(w2_scale, "w2_scale", torch.float32, (G, H // 128, I // 128))
+    y, ids, scales = (None,) * 3 if out is None else out
+    y = _out(y, "y", (T, H), x.dtype, d)
+    ids = _out(ids, "ids", (T, k), torch.int32, d)
+    scales = _out(scales, "scales", (T, k), torch.float32, d)
+    if ws is None:
+        ws = layer_few_workspace(T, H, I, E, k, n_shared, x.dtype, d)
+    _dev(ws, "ws", torch.uint8)
+    _call("moe_layer_few", d, x, _DT[x.dtype], logits, T, H, I, E, method, k, n_group, topk_group, bias,
+          float(scaling), ROUTE_FLAG_RENORMALIZE if renormalize else 0, n_shared, w13, w2, _DT[w13.dtype],
+          w13_scale, w2_scale, ids, scales, y, ws, ws.numel())
+    return y, ids, scales
 
 
 def timing_enable(on: bool = True):

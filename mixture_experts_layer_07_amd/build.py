@@ -13,7 +13,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmoe.so")
 SOURCES = ["api.hip", "route.hip", "permute.hip", "ffn.hip", "fused.hip", "finalize.hip",
-           "quant.hip", "noalloc.hip", "norm.hip", "dispatch.hip", "swiglu.hip", "route_backward.hip"]
+           "quant.hip", "noalloc.hip", "norm.hip", "dispatch.hip", "swiglu.hip", "route_backward.hip",
+           "mxfp4.hip", "few.hip"]
 CALIB_SOURCE = "calib.hip"
 CALIB_LIB = os.path.join(HERE, "libmoe_calib.so")
 MARSHAL_SOURCE = "marshal.cpp"

@@ -158,17 +158,19 @@ const char* moe_last_error(void) { return g_err; }
 size_t moe_workspace_size(int T, int k, int E, int n_shared, int H, int I, int act)
 {
     (void)H;
-    if (check_common(T, k, E, n_shared) != MOE_OK || I < 0 || !(valid_act(act) || act == MOE_FP8_E4M3))
+    if (check_common(T, k, E, n_shared) != MOE_OK || I < 0 ||
+        !(valid_act(act) || act == MOE_FP8_E4M3 || act == MOE_MXFP4))
         return 0;
     const size_t a = align256(permute_scratch_bytes(T, k, E));
     const size_t b = act == MOE_FP8_E4M3 ? ffn_fp8_scratch_bytes(T, k, n_shared, I)
+                     : act == MOE_MXFP4  ? ffn_mxfp4_scratch_bytes(T, k, n_shared, I)
                                          : ffn_scratch_bytes(T, k, n_shared, I, act);
     return (a > b ? a : b) + 256;
 }
 
-moe_status moe_route(const float* logits, int T, int E, int method, int k, int n_group,
-                     int topk_group, const float* bias, float scaling, unsigned flags,
-                     int32_t* ids, float* scales, void* stream)
+// Shape, method and settings of a routing (everything but its buffers).
+static moe_status check_route(int T, int E, int method, int k, int n_group, int topk_group, float scaling,
+                              unsigned flags)
 {
     moe_status st = check_common(T, k, E, 0);
     if (st != MOE_OK) return st;
@@ -190,13 +192,26 @@ moe_status moe_route(const float* logits, int T, int E, int method, int k, int n
         if (k > topk_group * gsz)
             return set_error(MOE_ERR_INVALID_ARG, "k=%d exceeds the experts of the kept groups (%d)", k, topk_group * gsz);
     }
+    return MOE_OK;
+}
+
+// The bias of the methods that have one.
+static const float* route_bias(int method, const float* bias)
+{
+    return (method == MOE_ROUTE_DEEPSEEKV3 || method == MOE_ROUTE_MINIMAX2) ? bias : nullptr;
+}
+
+moe_status moe_route(const float* logits, int T, int E, int method, int k, int n_group,
+                     int topk_group, const float* bias, float scaling, unsigned flags,
+                     int32_t* ids, float* scales, void* stream)
+{
+    moe_status st = check_route(T, E, method, k, n_group, topk_group, scaling, flags);
+    if (st != MOE_OK) return st;
     if (T == 0) return MOE_OK;
     if (!logits || !ids || !scales)
         return set_error(MOE_ERR_INVALID_ARG, "logits, ids and scales must be non-null");
-    return launch_route(logits, T, E, method, k, n_group, topk_group,
-                        (method == MOE_ROUTE_DEEPSEEKV3 || method == MOE_ROUTE_MINIMAX2) ? bias : nullptr,
-                        scaling, flags, ids,
-                        scales, static_cast<hipStream_t>(stream));
+    return launch_route(logits, T, E, method, k, n_group, topk_group, route_bias(method, bias), scaling, flags,
+                        ids, scales, static_cast<hipStream_t>(stream));
 }
 
 moe_status moe_permute(const int32_t* ids, int T, int k, int E, int n_shared,
@@ -636,6 +651,124 @@ moe_status moe_swiglu_backward(const void* dh, int dt, const uint8_t* guq, const
     if (is_any(d_gu, {dh, guq, gu_scale, h}) || is_any(h, {guq, gu_scale})) return same_buffer();
     if (!aligned16({dh, guq, d_gu, h})) return misaligned();
     return launch_swiglu_backward(dh, dt, guq, gu_scale, rows, I, d_gu, h, static_cast<hipStream_t>(stream));
+}
+
+// ------------------------------------------------------------------- MXFP4
+static moe_status check_mxfp4(int rows, int cols, int dt)
+{
+    moe_status st = check_rows("rows", rows);
+    if (st != MOE_OK) return st;
+    if (cols < 1) return set_error(MOE_ERR_INVALID_ARG, "cols must be positive (got %d)", cols);
+    if (cols % 32) return set_error(MOE_ERR_UNSUPPORTED, "cols must be a multiple of 32 (got %d)", cols);
+    if (!valid_act(dt)) return set_error(MOE_ERR_INVALID_ARG, "dtype %d must be MOE_F32 or MOE_BF16", dt);
+    return MOE_OK;
+}
+
+moe_status moe_quantize_mxfp4(const void* x, int dt, int rows, int cols, uint8_t* q, uint8_t* scale,
+                              void* stream)
+{
+    moe_status st = check_mxfp4(rows, cols, dt);
+    if (st != MOE_OK || rows == 0) return st;
+    if (!x || !q || !scale) return set_error(MOE_ERR_INVALID_ARG, "x, q and scale must be non-null");
+    if (is_any(x, {q, scale}) || is_any(q, {scale})) return same_buffer();
+    if (!aligned16({x, q})) return misaligned();
+    return launch_quantize_mxfp4(x, dt, rows, cols, q, scale, static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int rows, int cols, int dt, void* x,
+                                void* stream)
+{
+    moe_status st = check_mxfp4(rows, cols, dt);
+    if (st != MOE_OK || rows == 0) return st;
+    if (!q || !scale || !x) return set_error(MOE_ERR_INVALID_ARG, "q, scale and x must be non-null");
+    if (is_any(x, {q, scale})) return same_buffer();
+    if (!aligned16({x, q})) return misaligned();
+    return launch_dequantize_mxfp4(q, scale, rows, cols, dt, x, static_cast<hipStream_t>(stream));
+}
+
+moe_status moe_expert_ffn_mxfp4(const uint8_t* xq, const uint8_t* x_scale, int T, int H, int I, int k, int E,
+                                int n_shared, const int32_t* expert_offsets, const int32_t* permuted_pair,
+                                const uint8_t* w13, const uint8_t* w2, const uint8_t* w13_scale,
+                                const uint8_t* w2_scale, void* fc2_out, void* ws, size_t ws_bytes, void* stream)
+{
+    moe_status st = check_common(T, k, E, n_shared);
+    if (st != MOE_OK) return st;
+    if (H < 1 || I < 1) return set_error(MOE_ERR_INVALID_ARG, "H and I must be positive (H=%d, I=%d)", H, I);
+    if (H % 128 || I % 128)
+        return set_error(MOE_ERR_UNSUPPORTED, "H and I must be multiples of 128 (H=%d, I=%d)", H, I);
+    // offsets of codes and scales in bytes, of rows in 32 bits
+    const unsigned long long lim = 1ull << 32, rows = (unsigned long long)T * (k + n_shared);
+    if ((unsigned long long)T * (H / 2) >= lim || rows * (I / 2) >= lim || 2ull * I * (H / 2) >= lim)
+        return set_error(MOE_ERR_UNSUPPORTED, "xq, hq or one expert's weights exceed 4 GiB (T=%d, H=%d, I=%d)", T, H, I);
+    if (T == 0) return MOE_OK;
+    if (!xq || !x_scale || !expert_offsets || !permuted_pair || !w13 || !w2 || !w13_scale || !w2_scale || !fc2_out)
+        return set_error(MOE_ERR_INVALID_ARG,
+                         "xq, x_scale, expert_offsets, permuted_pair, w13, w2, their scales and fc2_out "
+                         "must be non-null");
+    if (is_any(fc2_out, {xq, x_scale, expert_offsets, permuted_pair, w13, w2, w13_scale, w2_scale, ws}) ||
+        is_any(ws, {xq, x_scale, expert_offsets, permuted_pair, w13, w2, w13_scale, w2_scale}))
+        return same_buffer();
+    if (!aligned16({xq, x_scale, w13, w2, w13_scale, w2_scale, fc2_out, ws}))
+        return set_error(MOE_ERR_INVALID_ARG, "codes, scales, fc2_out and the workspace must be 16-byte aligned");
+    const size_t need = ffn_mxfp4_scratch_bytes(T, k, n_shared, I);
+    if (!ws || ws_bytes < need)
+        return set_error(MOE_ERR_WORKSPACE, "expert_ffn_mxfp4 needs %zu workspace bytes (got %zu)", need, ws_bytes);
+    return launch_ffn_mxfp4(xq, x_scale, T, H, I, k, E, n_shared, expert_offsets, permuted_pair, w13, w2,
+                            w13_scale, w2_scale, fc2_out, ws, static_cast<hipStream_t>(stream));
+}
+
+// ---------------------------------------------------------- a few tokens
+static moe_status check_few(int T, int H, int I, int E, int k, int n_shared, int act, int wdt)
+{
+    moe_status st = check_common(T, k, E, n_shared);
+    if (st != MOE_OK) return st;
+    if (T > MOE_FEW_MAX_T)
+        return set_error(MOE_ERR_UNSUPPORTED, "T = %d exceeds the limit of layer_few, %d tokens", T, MOE_FEW_MAX_T);
+    if (H < 1 || I < 1) return set_error(MOE_ERR_INVALID_ARG, "H and I must be positive (H=%d, I=%d)", H, I);
+    if (H % 128 || I % 128)
+        return set_error(MOE_ERR_UNSUPPORTED, "H and I must be multiples of 128 (H=%d, I=%d)", H, I);
+    if (H > (1 << 20) || I > (1 << 20))
+        return set_error(MOE_ERR_UNSUPPORTED, "H = %d or I = %d exceeds 2^20", H, I);
+    if (!valid_act(act)) return set_error(MOE_ERR_INVALID_ARG, "activation dtype %d must be MOE_F32 or MOE_BF16", act);
+    if (wdt < MOE_F32 || wdt > MOE_MXFP4) return set_error(MOE_ERR_INVALID_ARG, "unknown weight dtype %d", wdt);
+    if ((act == MOE_F32) != (wdt == MOE_F32))
+        return set_error(MOE_ERR_UNSUPPORTED, "fp32 activations go with fp32 weights, bf16 ones with the others");
+    return MOE_OK;
+}
+
+size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int k, int n_shared, int act)
+{
+    if (check_few(T, H, I, E, k, n_shared, act, act) != MOE_OK) return 0;
+    return few_scratch_bytes(T, I, k, n_shared, act);
+}
+
+moe_status moe_layer_few(const void* x, int act, const float* logits, int T, int H, int I, int E, int method,
+                         int k, int n_group, int topk_group, const float* bias, float scaling, unsigned flags,
+                         int n_shared, const void* w13, const void* w2, int wdt, const void* w13_scale,
+                         const void* w2_scale, int32_t* ids, float* scales, void* y, void* ws, size_t ws_bytes,
+                         void* stream)
+{
+    moe_status st = check_few(T, H, I, E, k, n_shared, act, wdt);
+    if (st == MOE_OK) st = check_route(T, E, method, k, n_group, topk_group, scaling, flags);
+    if (st != MOE_OK || T == 0) return st;
+    if (!x || !logits || !w13 || !w2 || !ids || !scales || !y)
+        return set_error(MOE_ERR_INVALID_ARG, "x, logits, w13, w2, ids, scales and y must be non-null");
+    const bool scaled = wdt == MOE_FP8_E4M3 || wdt == MOE_MXFP4;
+    if (scaled && (!w13_scale || !w2_scale))
+        return set_error(MOE_ERR_INVALID_ARG, "8- and 4-bit weights need w13_scale and w2_scale");
+    if (!scaled) w13_scale = w2_scale = nullptr;
+    bias = route_bias(method, bias);
+    const std::initializer_list<const void*> in = {x, logits, bias, w13, w2, w13_scale, w2_scale};
+    if (is_any(y, in) || is_any(ids, in) || is_any(scales, in) || is_any(ws, in) || is_any(y, {ids, scales, ws}) ||
+        is_any(ids, {scales, ws}) || is_any(scales, {ws}))
+        return same_buffer();
+    if (!aligned16({x, w13, w2, w13_scale, w2_scale, y, ws}))
+        return set_error(MOE_ERR_INVALID_ARG, "x, the weights, their scales, y and the workspace must be 16-byte aligned");
+    const size_t need = few_scratch_bytes(T, I, k, n_shared, act);
+    if (!ws || ws_bytes < need)
+        return set_error(MOE_ERR_WORKSPACE, "layer_few needs %zu workspace bytes (got %zu)", need, ws_bytes);
+    return launch_layer_few(x, logits, T, H, I, E, method, k, n_group, topk_group, bias, scaling, flags, n_shared,
+                            w13, w2, wdt, w13_scale, w2_scale, ids, scales, y, ws, static_cast<hipStream_t>(stream));
 }
 
 moe_status moe_timing_enable(int enable)

@@ -129,6 +129,20 @@ moe_status launch_ffn_fp8(const uint8_t* xq, const float* x_scale, int T, int H,
                           int n_shared, const int32_t* offsets, const int32_t* permuted_pair,
                           const uint8_t* w13, const uint8_t* w2, const float* w13_scale,
                           const float* w2_scale, void* fc2_out, void* ws, hipStream_t s);
+size_t ffn_mxfp4_scratch_bytes(int T, int k, int n_shared, int I);
+moe_status launch_ffn_mxfp4(const uint8_t* xq, const uint8_t* x_scale, int T, int H, int I, int k, int E,
+                            int n_shared, const int32_t* offsets, const int32_t* permuted_pair,
+                            const uint8_t* w13, const uint8_t* w2, const uint8_t* w13_scale,
+                            const uint8_t* w2_scale, void* fc2_out, void* ws, hipStream_t s);
+moe_status launch_quantize_mxfp4(const void* x, int dt, int rows, int cols, uint8_t* q, uint8_t* scale,
+                                 hipStream_t s);
+moe_status launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int rows, int cols, int dt, void* x,
+                                   hipStream_t s);
+size_t few_scratch_bytes(int T, int I, int k, int n_shared, int act);
+moe_status launch_layer_few(const void* x, const float* logits, int T, int H, int I, int E, int method, int k,
+                            int n_group, int topk_group, const float* bias, float scaling, unsigned flags,
+                            int n_shared, const void* w13, const void* w2, int wdt, const void* w13_scale,
+                            const void* w2_scale, int32_t* ids, float* scales, void* y, void* ws, hipStream_t s);
 moe_status launch_ffn_fused(const void* x, const float* x_scale, int act, int T, int H, int I, int k,
                             int E, int n_shared, const int32_t* offsets, const int32_t* permuted_pair,
                             const void* w13, const void* w2, int wdt, const float* w13_scale,

@@ -102,6 +102,16 @@ __device__ __forceinline__ f32x4_t mfma_fp8(const i32x8_t& a, const i32x8_t& b)
                                                             127, 0, 127);
 }
 
+// 16x16x128 MFMA on e2m1 codes (format 4 for both operands), 32 a lane, with each
+// lane's E8M0 scale in byte B of its scale operand.
+template <int B>
+__device__ __forceinline__ f32x4_t mfma_mxfp4(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c, int sa, int sb)
+{
+    const i32x8_t wa = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+    const i32x8_t wb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, B, sa, B, sb);
+}
+
 // Lane group g's 32 fp8 codes of one row of a staged 128-byte K block: logical
 // chunks g and g+4 (K bytes [16g, 16g+16) and [64+16g, 64+16g+16)).  The MFMA
 // sums over the whole block, so any assignment of K positions to lane groups

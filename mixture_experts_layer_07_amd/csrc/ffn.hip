@@ -45,6 +45,7 @@
 
 #include "common.h"
 #include "dma.h"
+#include "mxfp4.h"
 
 namespace moe {
 namespace {
@@ -54,9 +55,9 @@ enum Mode { FC1 = 0, FC2 = 1 };
 struct FfnArgs {
     const char* a_src;         // FC1: x [T, H];  FC2: h [R, I]
     const char* w;             // FC1: w13 [G, 2I, H];  FC2: w2 [G, H, I]
-    const float* wscale;       // fp8 block scales or null
-    const float* ascale;       // fp8 activations: FC1 x scales [T, H/128], FC2 h scales [R, I/128]
-    float* out_scale;          // fp8 activations, FC1: h scales [R, I/128] out
+    const void* wscale;        // block scales (fp8: fp32; MXFP4: a byte each) or null
+    const void* ascale;        // scales of the activations: fp8 x [T, H/128], h [R, I/128]; MXFP4 [.., K/32] bytes
+    void* out_scale;           // 8- and 4-bit activations, FC1: the scales of h out
     char* out;                 // FC1: h [R, I];  FC2: fc2_out [R, H]
     const int32_t* offsets;    // [G + 1]
     const int32_t* permuted_pair;
@@ -448,32 +449,53 @@ __global__ __launch_bounds__(C::NT) void grouped_gemm_kernel(FfnArgs a)
 // scale), software-pipelined one MFMA behind.  FC1's epilogue quantises h per
 // row and 128 intermediate channels (one 256-column tile holds exactly one
 // such block of every row).
-template <int BM_, int BN_, int WM_, int WN_, int GM_, int S_, bool W8_ = false, bool A8_ = false>
+//
+// MXFP4 activations and weights (A4): a stage is 256 K values, 128-byte rows of
+// codes for both operands, two K-steps of v_mfma_f32_16x16x128_f8f6f4 that take
+// the scales themselves (one E8M0 byte a lane: a lane feeds 32 values of a row,
+// one scale block).  Its sums are good for fp32: products of e2m1 codes are small
+// integers, and chains of 64 steps over random scales came out 30 times nearer
+// to the exact sum than fp32 additions in order (3e-7 of the result's norm), so
+// blocks accumulate in the instruction.  Lane group g of K-step b takes 32-value
+// block 2g + b, so that a lane's two scales are neighbouring bytes: one 2-byte
+// LDS read a row for both steps, selected by the instruction (op_sel).  The
+// staged order of a row's 16-byte chunks is permuted to match (virtual chunk
+// 4b + g holds block 2g + b), and then swizzled like the others.  The scales of
+// the stage's BM + BN rows, 8 bytes each, are staged by 4-byte transfers spread
+// over the waves.  K is a multiple of 128: in a last stage of 128 values lane
+// groups 2 and 3 read what groups 0 and 1 read, and their activations count as
+// zeros.  FC1's epilogue quantises h per row and 32 channels inside a wave; the
+// staged weight rows are ordered so that a lane holds eight neighbouring ones.
+template <int BM_, int BN_, int WM_, int WN_, int GM_, int S_, bool W8_ = false, bool A8_ = false, bool A4_ = false>
 struct DmaCfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GM = GM_, S = S_;
     static constexpr bool A8 = A8_;
+    static constexpr bool A4 = A4_;
     static constexpr bool W8 = W8_ || A8_;                 // fp8 weights
     static constexpr bool WNARROW = W8 && !A8;             // fp8 weights widened to bf16
     static constexpr int NT = WM * WN * 64;
     static constexpr int NW = WM * WN;
-    static constexpr int BK = A8 ? 128 : 64;               // K per stage
-    static constexpr int KSTEPS = A8 ? 1 : BK / 32;        // MFMA K-steps per stage
+    static constexpr int BK = A4 ? 256 : A8 ? 128 : 64;    // K per stage
+    static constexpr int KSTEPS = A8 ? 1 : A4 ? 2 : BK / 32;  // MFMA K-steps per stage
     static constexpr int BROWB = WNARROW ? 64 : 128;       // weight bytes per staged row
     static constexpr int A_OPS = BM / 8;                   // 1 KB DMA ops per stage, activations
     static constexpr int B_OPS = BN * BROWB / 1024;        // ... and weights
     static constexpr int A_BYTES = BM * 128;
     static constexpr int B_BYTES = BN * BROWB;
-    static constexpr int SA_BYTES = A8 ? NW * 256 : 0;     // per-wave activation-scale slots
+    static constexpr int S_OPS = A4 ? (BM + BN) / 32 : 0;  // 256-byte scale transfers per stage
+    static constexpr int IPW_S = A4 ? (S_OPS + NW - 1) / NW : A8 ? 1 : 0;  // ... per wave
+    static constexpr int SA_BYTES = A8 ? NW * 256 : S_OPS * 256;  // A8: per-wave slots
     static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES;  // bytes per stage
     static constexpr int NINS = A_OPS + B_OPS;
     static constexpr int IPW_AB = NINS / NW;               // 1 KB ops per wave per stage
-    static constexpr int IPW = IPW_AB + (A8 ? 1 : 0);      // ... plus the scale transfer
+    static constexpr int IPW = IPW_AB + IPW_S;             // ... plus the scale transfers
     static constexpr int WTM = BM / WM, WTN = BN / WN;
     static constexpr int MI = WTM / 16, NI = WTN / 16;
     static constexpr int AMAX_BYTES = A8 ? BM * WN * 4 : 4;  // FC1 epilogue: row maxima per wave column
     static_assert(BM % 8 == 0 && NINS % NW == 0 && IPW_AB >= 1, "DMA ops split evenly over waves");
     static_assert(WTM % 16 == 0 && WTN % 32 == 0, "tile");
     static_assert(!A8 || (WTM <= 64 && BN == 256), "A8: one scale transfer per wave; 128 h columns per tile");
+    static_assert(!A4 || (!W8_ && !A8 && BM % 32 == 0 && WTN % 64 == 0), "A4: whole scale transfers; 32 h columns per wave");
     static_assert(S >= 2 && S <= 8 && S * STAGE + AMAX_BYTES <= 156 * 1024,
                   "ring (LDS also holds the tile tables)");
 };
@@ -528,8 +550,10 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
     int tile = slot;
     if (tile >= total) return;
 
-    const int nk = a.K / C::BK;
-    const size_t a_ld = (size_t)a.K * (C::A8 ? 1 : 2), w_ld = (size_t)a.K * (C::W8 ? 1 : 2);
+    const int nk = C::A4 ? (a.K + C::BK - 1) / C::BK : a.K / C::BK;
+    const bool half_last = C::A4 && a.K % C::BK != 0;  // A4: the last stage holds 128 values
+    const size_t a_ld = C::A4 ? (size_t)a.K / 2 : (size_t)a.K * (C::A8 ? 1 : 2);
+    const size_t w_ld = C::A4 ? (size_t)a.K / 2 : (size_t)a.K * (C::W8 ? 1 : 2);
     const unsigned lds_base = (unsigned)(size_t)(__attribute__((address_space(3))) char*)lds;
 
     // Op o = q*NW + wave of a stage (wave-uniform, q < IPW_AB) stages
@@ -540,7 +564,11 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
     // holds logical chunk physical ^ swizzle(row).  With fp8 activations op
     // q = IPW_AB of every wave stages the activation scales of the wave's own
     // rows: lane l fetches the scale of row wm*WTM + l % WTM.
-    auto op_is_s = [&](int q) { return C::A8 && q == C::IPW_AB; };
+    // A4's scale op o (of S_OPS, spread over the waves; the last ones may be done
+    // twice) stages the 8 bytes of activation rows 32o .. 32o+31, then of weight
+    // rows: lane l half l % 2 of row l / 2.
+    auto op_is_s = [&](int q) { return (C::A8 || C::A4) && q >= C::IPW_AB; };
+    auto s_op = [&](int q) { return min((q - C::IPW_AB) * C::NW + wave, C::S_OPS - 1); };
     auto op_is_a = [&](int q) { return q < C::IPW_AB && q * C::NW + wave < C::A_OPS; };
     auto op_row = [&](int q) {  // A row, or B row, of this lane in op q < IPW_AB
         const int o = q * C::NW + wave;
@@ -548,17 +576,34 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
         return C::WNARROW ? (o - C::A_OPS) * 16 + (lane >> 2) : (o - C::A_OPS) * 8 + (lane >> 3);
     };
     auto op_chunk = [&](int q, int row) {  // logical 16-byte chunk this lane fetches
+        if constexpr (C::A4) {
+            const int v = (lane & 7) ^ (row & 7);  // virtual chunk 4b + g: block 2g + b
+            return 2 * (v & 3) + (v >> 2);
+        }
         if (op_is_a(q) || !C::WNARROW) return (lane & 7) ^ (row & 7);
         return (lane & 3) ^ ((row >> 2) & 3);
     };
-    const int s_row = wm * C::WTM + lane % C::WTM;  // scale op: this lane's tile row
+    auto s_row = [&](int q) {  // scale op: this lane's tile row (A4: past BM, weight rows)
+        return C::A4 ? s_op(q) * 32 + (lane >> 1) : wm * C::WTM + lane % C::WTM;
+    };
+    // the weight row that row j of the staged B tile holds
+    auto weight_row = [&](const TileInfo& ti, int j) {
+        if (MODE == FC1) {
+            const int blk = j >> 4, pair = blk >> 1, r = j & 15;
+            // A4: rows 4g + i of pairs 2b and 2b + 1 are channels 8g + i and 8g + 4 + i of block b
+            const int col = ti.nt * (C::BN / 2) +
+                            (C::A4 ? (pair >> 1) * 32 + (r >> 2) * 8 + (pair & 1) * 4 + (r & 3) : pair * 16 + r);
+            return (blk & 1) ? a.I + col : col;
+        }
+        return min(ti.nt * C::BN + j, a.N - 1);  // partial last N-tile
+    };
 
     // For FC1 A rows the token comes from permuted_pair: a_raw() only loads the
     // entry (from an always-valid address) and source() interprets it, so the
     // next tile's loads can be issued early and consumed a whole tile later.
     auto a_raw = [&](const TileInfo& ti, int q) -> int {
         if (MODE == FC2 || !(op_is_a(q) || op_is_s(q))) return 0;
-        const int rr = ti.m0 + (op_is_s(q) ? s_row : op_row(q));
+        const int rr = ti.m0 + (op_is_s(q) ? s_row(q) : op_row(q));
         const int i = (ti.g < a.E && rr < ti.nrows) ? ti.row0 + rr : 0;
         // global-space load: a flat load would also count in lgkmcnt and make
         // the LDS-only barriers wait for it
@@ -568,7 +613,9 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
     // (a_src), this tile's group of weights (wbase) or the activation scales.
     auto source = [&](const TileInfo& ti, int q, int raw) -> uint32_t {
         if (op_is_s(q)) {
-            const int rr = ti.m0 + s_row;
+            if (C::A4 && s_op(q) * 32 >= C::BM)
+                return (uint32_t)weight_row(ti, s_row(q) - C::BM) * (uint32_t)(a.K / 32) + (lane & 1) * 4;
+            const int rr = ti.m0 + s_row(q);
             long r;
             if (MODE == FC1) {
                 const int tok = (rr >= ti.nrows) ? 0 : (ti.g < a.E ? raw / a.k : rr);
@@ -576,6 +623,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
             } else {
                 r = ti.row0 + (rr < ti.nrows ? rr : 0);
             }
+            if constexpr (C::A4) return (uint32_t)(r * (a.K / 32)) + (lane & 1) * 4;
             return (uint32_t)(r * (a.K / 128) * 4);
         }
         const int row = op_row(q);
@@ -591,29 +639,34 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
             }
             p = (uint32_t)(r * a_ld);
         } else {
-            const int j = row;
-            int wrow;
-            if (MODE == FC1) {
-                const int blk = j >> 4, pair = blk >> 1;
-                const int col = ti.nt * (C::BN / 2) + pair * 16 + (j & 15);
-                wrow = (blk & 1) ? a.I + col : col;
-            } else {
-                wrow = min(ti.nt * C::BN + j, a.N - 1);  // partial last N-tile
-            }
-            p = (uint32_t)(wrow * w_ld);
+            p = (uint32_t)(weight_row(ti, row) * w_ld);
         }
         return p + op_chunk(q, row) * 16;
     };
     auto group_weights = [&](const TileInfo& ti) { return uniform_ptr(a.w + (size_t)ti.g * a.N * w_ld); };
     const char* abase = uniform_ptr(a.a_src);
     const char* sbase = uniform_ptr(reinterpret_cast<const char*>(a.ascale));
+    auto group_scales = [&](const TileInfo& ti) {  // A4 only
+        return uniform_ptr(reinterpret_cast<const char*>(a.wscale) + (size_t)ti.g * a.N * (a.K / 32));
+    };
     const char* wbase;  // weights of the group whose slices `issue` sends
+    const char* wsbase = nullptr;  // ... and their scales
     uint32_t src[C::IPW];
+    // A4: what a lane of groups 2 and 3 goes back in a last stage of 128 values
+    const uint32_t back = C::A4 && op_chunk(0, lane >> 3) >= 4 ? 64 : 0, sback = (lane & 1) * 4;
     auto issue = [&](int st, int kt) {
+        const bool half = half_last && kt == nk - 1;
 #pragma unroll
         for (int q = 0; q < C::IPW_AB; ++q)
             dma16(__builtin_amdgcn_readfirstlane(lds_base + st * C::STAGE + (q * C::NW + wave) * 1024),
-                  op_is_a(q) ? abase : wbase, src[q] + (uint32_t)kt * (op_is_a(q) ? 128u : (uint32_t)C::BROWB));
+                  op_is_a(q) ? abase : wbase,
+                  src[q] + (uint32_t)kt * (op_is_a(q) ? 128u : (uint32_t)C::BROWB) - (half ? back : 0u));
+        if constexpr (C::A4) {
+#pragma unroll
+            for (int q = C::IPW_AB; q < C::IPW; ++q)
+                dma4(__builtin_amdgcn_readfirstlane(lds_base + st * C::STAGE + C::A_BYTES + C::B_BYTES + s_op(q) * 256),
+                     s_op(q) * 32 < C::BM ? sbase : wsbase, src[q] + (uint32_t)kt * 8u - (half ? sback : 0u));
+        }
         if constexpr (C::A8)
             dma4(__builtin_amdgcn_readfirstlane(lds_base + st * C::STAGE + C::A_BYTES + C::B_BYTES + wave * 256),
                  sbase, src[C::IPW_AB] + (uint32_t)kt * 4u);
@@ -630,6 +683,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
 #pragma unroll
         for (int q = 0; q < C::IPW; ++q) src[q] = source(cur, q, idx[q]);
         wbase = group_weights(cur);
+        if constexpr (C::A4) wsbase = group_scales(cur);
     }
     int ring = 0;  // ring slot of the current tile's slice 0
 #pragma unroll
@@ -715,6 +769,38 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                     }
                     __builtin_amdgcn_sched_barrier(0);
                 }
+            } else if constexpr (C::A4) {
+                const int g4 = lane >> 4;
+                const char* ls = lb + C::B_BYTES;
+                const bool none = half_last && kt == nk - 1 && g4 >= 2;  // past the row's end
+                int sa[C::MI], sw[C::NI];
+#pragma unroll
+                for (int mi = 0; mi < C::MI; ++mi)
+                    sa[mi] = *reinterpret_cast<const uint16_t*>(ls + (wm * C::WTM + mi * 16 + (lane & 15)) * 8 + g4 * 2);
+#pragma unroll
+                for (int ni = 0; ni < C::NI; ++ni)
+                    sw[ni] = *reinterpret_cast<const uint16_t*>(
+                        ls + (C::BM + wn * C::WTN + ni * 16 + (lane & 15)) * 8 + g4 * 2);
+                auto kstep = [&](auto step) {
+                    constexpr int b = decltype(step)::value;
+                    u32x4_t fa[C::MI];
+#pragma unroll
+                    for (int mi = 0; mi < C::MI; ++mi) {
+                        fa[mi] = *reinterpret_cast<const u32x4_t*>(
+                            la + dma_off(wm * C::WTM + mi * 16 + (lane & 15), 4 * b + g4));
+                        if (none) fa[mi] = u32x4_t{0u, 0u, 0u, 0u};
+                    }
+#pragma unroll
+                    for (int ni = 0; ni < C::NI; ++ni) {
+                        const u32x4_t fb = *reinterpret_cast<const u32x4_t*>(
+                            lb + dma_off(wn * C::WTN + ni * 16 + (lane & 15), 4 * b + g4));
+#pragma unroll
+                        for (int mi = 0; mi < C::MI; ++mi)
+                            acc[mi][ni] = mfma_mxfp4<b>(fb, fa[mi], acc[mi][ni], sw[ni], sa[mi]);
+                    }
+                };
+                kstep(std::integral_constant<int, 0>());
+                kstep(std::integral_constant<int, 1>());
             } else {
 #pragma unroll
             for (int ks = 0; ks < C::KSTEPS; ++ks) {
@@ -783,6 +869,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
 #pragma unroll
             for (int q = 0; q < C::IPW; ++q) src[q] = source(nxt, q, nidx[q]);
             wbase = group_weights(nxt);
+            if constexpr (C::A4) wsbase = group_scales(nxt);
             ring = (ring + nk) % C::S;
 #pragma unroll
             for (int st = 0; st < C::S - 1; ++st)
@@ -841,7 +928,38 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                         const int col = cur.nt * (C::BN / 2) + ((wn * C::WTN) / 32 + q) * 16 + ecol;
                         *(__attribute__((address_space(1))) uint32_t*)(hq + r * a.I + col) = fp8x4_code(hv, sc);
                     }
-                    if (wn == 0 && lane < 16) a.out_scale[r * sk_out + cur.nt] = sc;
+                    if (wn == 0 && lane < 16) static_cast<float*>(a.out_scale)[r * sk_out + cur.nt] = sc;
+                }
+            }
+        } else if (MODE == FC1 && C::A4) {
+            // h -> MXFP4 per row and 32 channels: pairs 2b and 2b + 1 of this wave,
+            // eight channels in each of the four lanes that share a row
+            uint8_t* hq = reinterpret_cast<uint8_t*>(a.out);
+            uint8_t* hs = reinterpret_cast<uint8_t*>(a.out_scale);
+#pragma unroll
+            for (int mi = 0; mi < C::MI; ++mi) {
+                const int rr = cur.m0 + wm * C::WTM + mi * 16 + erow;
+                const size_t r = (size_t)(cur.row0 + rr);
+#pragma unroll
+                for (int b = 0; b < C::NI / 4; ++b) {
+                    float hv[8];
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float gt = acc[mi][4 * b + (i >> 2) * 2][i & 3];
+                        const float up = acc[mi][4 * b + (i >> 2) * 2 + 1][i & 3];
+                        hv[i] = gt * __builtin_amdgcn_rcpf(1.0f + expf(-gt)) * up;
+                        m = max(m, __float_as_uint(hv[i]) & 0x7fffffffu);
+                    }
+                    m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+                    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+                    const uint32_t sc = mxfp4_scale(m);
+                    if (rr < cur.nrows) {
+                        const int blk = cur.nt * (C::BN / 64) + wn * (C::WTN / 64) + b;  // of the row's I / 32
+                        *(__attribute__((address_space(1))) uint32_t*)(hq + r * (a.I / 2) + blk * 16 + (lane >> 4) * 4) =
+                            mxfp4_codes(hv, sc);
+                        if (lane < 16) hs[r * (a.I / 32) + blk] = (uint8_t)sc;
+                    }
                 }
             }
         } else if (MODE == FC1) {
@@ -1048,6 +1166,15 @@ moe_status run_classes_a8(const FfnArgs& f, int R, hipStream_t s, int kid)
                            DmaCfg<256, 256, 4, 2, 4, 2, true, true>>(f, R, s, kid);
 }
 
+// MXFP4 activations and weights.
+template <int MODE>
+moe_status run_classes_a4(const FfnArgs& f, int R, hipStream_t s, int kid)
+{
+    return run_classes_dma<MODE, DmaCfg<32, 256, 1, 4, 2, 4, false, false, true>,
+                           DmaCfg<128, 256, 2, 4, 2, 3, false, false, true>,
+                           DmaCfg<256, 256, 2, 4, 4, 2, false, false, true>>(f, R, s, kid);
+}
+
 // fp32 (small reference-precision layers): one 32x128 tile shape for all groups.
 template <>
 moe_status run_ffn<float, float>(const FfnArgs& fc1, const FfnArgs& fc2, int R, hipStream_t s)
@@ -1099,6 +1226,45 @@ moe_status launch_ffn_fp8(const uint8_t* xq, const float* x_scale, int T, int H,
     moe_status st = run_classes_a8<FC1>(f1, R, s, MOE_KID_FC1);
     if (st != MOE_OK) return st;
     return run_classes_a8<FC2>(f2, R, s, MOE_KID_FC2);
+}
+
+size_t ffn_mxfp4_scratch_bytes(int T, int k, int n_shared, int I)
+{
+    const size_t R = (size_t)T * k + (size_t)n_shared * T;
+    return align256(R * (size_t)(I / 2)) + align256(R * (size_t)(I / 32));
+}
+
+moe_status launch_ffn_mxfp4(const uint8_t* xq, const uint8_t* x_scale, int T, int H, int I, int k, int E,
+                            int n_shared, const int32_t* offsets, const int32_t* permuted_pair,
+                            const uint8_t* w13, const uint8_t* w2, const uint8_t* w13_scale,
+                            const uint8_t* w2_scale, void* fc2_out, void* ws, hipStream_t s)
+{
+    const int G = E + n_shared;
+    const int R = T * k + n_shared * T;
+    char* hq = static_cast<char*>(ws);
+    char* hs = hq + align256((size_t)R * (I / 2));
+    FfnArgs f1{};
+    f1.a_src = reinterpret_cast<const char*>(xq);
+    f1.ascale = x_scale;
+    f1.w = reinterpret_cast<const char*>(w13);
+    f1.wscale = w13_scale;
+    f1.out = hq;
+    f1.out_scale = hs;
+    f1.offsets = offsets;
+    f1.permuted_pair = permuted_pair;
+    f1.T = T; f1.k = k; f1.E = E; f1.G = G; f1.I = I;
+    f1.N = 2 * I; f1.K = H; f1.out_ld = I;
+    FfnArgs f2 = f1;
+    f2.a_src = hq;
+    f2.ascale = hs;
+    f2.w = reinterpret_cast<const char*>(w2);
+    f2.wscale = w2_scale;
+    f2.out = static_cast<char*>(fc2_out);
+    f2.out_scale = nullptr;
+    f2.N = H; f2.K = I; f2.out_ld = H;
+    moe_status st = run_classes_a4<FC1>(f1, R, s, MOE_KID_FC1);
+    if (st != MOE_OK) return st;
+    return run_classes_a4<FC2>(f2, R, s, MOE_KID_FC2);
 }
 
 size_t ffn_scratch_bytes(int T, int k, int n_shared, int I, int act)

@@ -188,6 +188,10 @@ Entry g_entries[] = {
     MOE_ENTRY(moe_route_backward, false),
     MOE_ENTRY(moe_swiglu, true),
     MOE_ENTRY(moe_swiglu_backward, false),
+    MOE_ENTRY(moe_quantize_mxfp4, false),
+    MOE_ENTRY(moe_dequantize_mxfp4, false),
+    MOE_ENTRY(moe_expert_ffn_mxfp4, false),
+    MOE_ENTRY(moe_layer_few, false),
 };
 
 // A tensor without storage of its own makes torch throw: no exception leaves
