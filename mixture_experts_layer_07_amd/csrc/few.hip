@@ -13,14 +13,17 @@
 //
 // A workgroup of eight waves takes 16 columns (of h: 16 gate and 16 up rows of the
 // weights) at a time; the waves share out the reduction length in pieces and add
-// their sums through LDS.  Weights go from memory to registers, 16 bytes a lane, the
-// next piece's loads in flight while a piece is multiplied; 16 rows of a column
-// tile are the first operand of the MFMA, up to 16 of the expert's tokens the
-// second (rows past the last token repeat it: a column of the result depends on
-// its own token alone).  An expert with more tokens is taken in chunks of 16.
+// their sums through LDS.  Weights go from memory to registers, the next pieces'
+// loads in flight while a piece is multiplied, 128 whole bytes of a row in eight lanes
+// (a lane's own row, 64 bytes of 16 rows a load, is what the MFMA takes, but streams
+// 4.5 TB/s where this does 6: the lanes of a wave exchange a piece through LDS of
+// their own).  The 16 rows of a column tile are the first operand of the MFMA, up
+// to 16 of the expert's tokens the second (rows past the last token repeat it: a
+// column of the result depends on its own token alone).  An expert with more
+// tokens is taken in chunks of 16.
 // MFMA forms: fp32 16x16x4, else bf16 16x16x32; e4m3 codes are widened to bf16 (exact)
 // and each 128-wide block's sum is scaled in fp32, MXFP4 codes with their scales (exact).
-// A lane feeds the K positions that its own 16 weight bytes hold, and loads the
+// A lane feeds the K positions that 16 bytes of its weight row hold, and loads the
 // same positions of its token.
 #include <math.h>
 
@@ -134,11 +137,24 @@ __device__ __forceinline__ int token_of(const FewArgs& a, const Tables& tb, cons
 }
 
 // ---------------------------------------------------------------- pieces
+// Memory as the buffer instructions address it: a scalar base, a scalar offset and
+// one of the lane's, so that no lane holds a pointer.
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer make_buffer(const char* p)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_ptr(p)), 0, 0xffffffffu, 0x00020000);
+}
+template <bool NT>  // NT: streamed past the caches
+__device__ __forceinline__ u32x4_t load16(Buffer b, uint32_t lane_offset, uint32_t offset)
+{
+    return __builtin_amdgcn_raw_buffer_load_b128(b, lane_offset, offset, NT ? 2 : 0);
+}
+
 // One piece: PE values of K of NR weight tiles (16 rows each) and of the tokens.
 template <class WT> struct Form;
 template <> struct Form<float> {
     using act = float;
-    static constexpr int kPE = 64, kPerLoad = 16;  // K values of a piece, and of one 16-byte load of a row's four lanes
+    static constexpr int kPE = 64, kPerLoad = 16;  // K values of a piece, and of 64 bytes of a row
     static constexpr int kDepth = 2;               // pieces in registers: one multiplied, the others on their way
     static constexpr int bytes(int n) { return n * 4; }
 };
@@ -156,8 +172,8 @@ template <> struct Form<fp8_t> {
 };
 template <> struct Form<fp4_t> {
     using act = bf16_t;
-    static constexpr int kPE = 128, kPerLoad = 128;
-    static constexpr int kDepth = 4;
+    static constexpr int kPE = 256, kPerLoad = 128;
+    static constexpr int kDepth = 2;
     static constexpr int bytes(int n) { return n / 2; }
 };
 
@@ -165,78 +181,103 @@ template <class WT, int NR>
 struct Piece {
     using F = Form<WT>;
     using act = typename F::act;
-    static constexpr int WL = F::kPE / F::kPerLoad;                 // weight loads of a tile
-    static constexpr int PL = F::kPerLoad / 4 * (int)sizeof(act) / 16;  // 16-byte activation loads for each of them
-    u32x4_t w[NR][WL];
+    static constexpr int RB = F::bytes(F::kPE);                     // bytes of a row
+    static constexpr int WL = RB / 64;                              // weight fragments of a tile
+    static constexpr int PL = F::kPerLoad / 4 * (int)sizeof(act) / 16;  // activation fragments for each of them
+    static constexpr int kStage = NR * 16 * RB;                     // LDS bytes of the exchange
+    u32x4_t w[NR][WL];  // load j: rows 8 (j % 2) + lane / 8, bytes 128 (j / 2) + 16 (lane % 8)
     u32x4_t v[WL][PL];
-    float s[NR];       // fp8: the block's scale
-    uint32_t s4[NR];   // MXFP4: the four scale bytes of the lane's row
+    float s[NR];            // fp8: the block's scale
+    uint32_t s4[NR][2];     // MXFP4: the eight scale bytes of the lane's row
 
-    // Piece p from the tiles' first rows (scalar; tile i `stride` bytes on) and the
-    // activations (scalar), with the lane's byte offsets in both.
-    __device__ __forceinline__ void load(const char* wbase, size_t stride, uint32_t woff, const char* vbase, uint32_t voff,
-                                         int p)
+    // The piece at scalar byte offset `wat` of an expert's weights (tile i `stride`
+    // bytes on, rows ld bytes apart) and `vat` of the activations, with the lane's
+    // offsets in both.  HALF: the row ends after half of the piece (MXFP4); the
+    // weights and activations of the first half stand in for the other one.
+    template <bool HALF>
+    __device__ __forceinline__ void load(Buffer wb, uint32_t wat, uint32_t stride, uint32_t ld, uint32_t woff, Buffer vb,
+                                         uint32_t vat, uint32_t voff)
     {
-        const char* wp = uniform_ptr(wbase + F::bytes(p * F::kPE));
-        const char* vp = uniform_ptr(vbase + (size_t)p * F::kPE * sizeof(act));
+        const uint32_t back = HALF && (threadIdx.x & 4) ? RB / 2 : 0;  // lanes of the second 64 bytes
 #pragma unroll
         for (int i = 0; i < NR; ++i)
 #pragma unroll
             for (int j = 0; j < WL; ++j)
-                w[i][j] = __builtin_nontemporal_load((const __attribute__((address_space(1))) u32x4_t*)(
-                    wp + i * stride + woff + F::bytes(j * F::kPerLoad)));
+                w[i][j] = load16<true>(wb, woff - back + (j >> 1) * 128, wat + i * stride + (j & 1) * 8 * ld);
 #pragma unroll
         for (int j = 0; j < WL; ++j)
 #pragma unroll
             for (int i = 0; i < PL; ++i)
-                v[j][i] = *(const __attribute__((address_space(1))) u32x4_t*)(
-                    vp + voff + j * F::kPerLoad * (int)sizeof(act) + i * 16);
+                v[j][i] = load16<false>(vb, voff + (HALF ? 0 : j) * F::kPerLoad * (int)sizeof(act) + i * 16, vat);
     }
 
-    __device__ __forceinline__ void add(f32x4_t (&acc)[NR], int g) const
+    // Lane l's rows become fragments: tile row l % 16, chunk 4 (j % 2) + l / 16 of 128 bytes.
+    __device__ __forceinline__ void exchange(char* stage, int lane, u32x4_t (&f)[NR][WL]) const
     {
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int j = 0; j < WL; ++j)
+                *reinterpret_cast<u32x4_t*>(stage + (i * (WL / 2) + (j >> 1)) * 2048 +
+                                            dma_off((j & 1) * 8 + (lane >> 3), lane & 7)) = w[i][j];
+        wave_lds_fence();
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+            for (int j = 0; j < WL; ++j)
+                f[i][j] = *reinterpret_cast<const u32x4_t*>(stage + (i * (WL / 2) + (j >> 1)) * 2048 +
+                                                            dma_off(lane & 15, (j & 1) * 4 + (lane >> 4)));
+    }
+
+    // HALF: of the second half nothing.
+    template <bool HALF>
+    __device__ __forceinline__ void add(f32x4_t (&acc)[NR], char* stage, int lane) const
+    {
+        u32x4_t f[NR][WL];
+        exchange(stage, lane, f);
+        constexpr int N = HALF ? WL / 2 : WL;
         if constexpr (std::is_same_v<WT, float>) {
 #pragma unroll
-            for (int j = 0; j < WL; ++j)
+            for (int j = 0; j < N; ++j)
 #pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[i][j].x), __uint_as_float(v[j][0].x), acc[i], 0, 0, 0);
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[i][j].y), __uint_as_float(v[j][0].y), acc[i], 0, 0, 0);
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[i][j].z), __uint_as_float(v[j][0].z), acc[i], 0, 0, 0);
-                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(w[i][j].w), __uint_as_float(v[j][0].w), acc[i], 0, 0, 0);
-                }
+                for (int i = 0; i < NR; ++i)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(f[i][j][c]), __uint_as_float(v[j][0][c]),
+                                                                      acc[i], 0, 0, 0);
         } else if constexpr (std::is_same_v<WT, bf16_t>) {
 #pragma unroll
-            for (int j = 0; j < WL; ++j)
+            for (int j = 0; j < N; ++j)
 #pragma unroll
-                for (int i = 0; i < NR; ++i) acc[i] = mfma_frag(w[i][j], v[j][0], acc[i], bf16_t());
+                for (int i = 0; i < NR; ++i) acc[i] = mfma_frag(f[i][j], v[j][0], acc[i], bf16_t());
         } else if constexpr (std::is_same_v<WT, fp8_t>) {
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 f32x4_t part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < WL; ++j) {
-                    part = mfma_frag(fp8x8_to_bf16x8(w[i][j].x, w[i][j].y), v[j][0], part, bf16_t());
-                    part = mfma_frag(fp8x8_to_bf16x8(w[i][j].z, w[i][j].w), v[j][1], part, bf16_t());
+                for (int j = 0; j < N; ++j) {
+                    part = mfma_frag(fp8x8_to_bf16x8(f[i][j].x, f[i][j].y), v[j][0], part, bf16_t());
+                    part = mfma_frag(fp8x8_to_bf16x8(f[i][j].z, f[i][j].w), v[j][1], part, bf16_t());
                 }
                 acc[i] += s[i] * part;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < WL; ++j)
+            for (int j = 0; j < N; ++j)
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
-                    const uint32_t sc = (s4[i] >> (8 * g)) & 0xffu;
+                    const uint32_t sc = (s4[i][j] >> (8 * (lane >> 4))) & 0xffu;
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        acc[i] = mfma_frag(mxfp4_to_bf16x8(w[i][j][q], sc), v[j][q], acc[i], bf16_t());
+                        acc[i] = mfma_frag(mxfp4_to_bf16x8(f[i][j][q], sc), v[j][q], acc[i], bf16_t());
                 }
         }
     }
 };
 
-// The scales of piece p of NR tiles: fp8, one value a tile (scalar); MXFP4, four bytes of the lane's row.
-template <class WT, int NR>
+// The scales of piece p of NR tiles whose first rows are row[]: fp8, one value a tile
+// (scalar); MXFP4, eight bytes of the lane's row (HALF: four).
+template <bool HALF, class WT, int NR>
 __device__ __forceinline__ void load_scales(Piece<WT, NR>& r, const void* scale, int e, int N, int K, const int (&row)[NR],
                                             int p, int lane)
 {
@@ -245,12 +286,28 @@ __device__ __forceinline__ void load_scales(Piece<WT, NR>& r, const void* scale,
 #pragma unroll
         for (int i = 0; i < NR; ++i) r.s[i] = s[((size_t)e * (N / 128) + row[i] / 128) * (K / 128) + p];
     } else if constexpr (std::is_same_v<WT, fp4_t>) {
-        const char* s = static_cast<const char*>(scale);
+        const Buffer b = make_buffer(static_cast<const char*>(scale) + (size_t)e * N * (K / 32));
 #pragma unroll
         for (int i = 0; i < NR; ++i)
-            r.s4[i] = *(const __attribute__((address_space(1))) uint32_t*)(
-                uniform_ptr(s + ((size_t)e * N + row[i]) * (K / 32) + p * 4) + (uint32_t)(lane & 15) * (uint32_t)(K / 32));
+#pragma unroll
+            for (int j = 0; j < (HALF ? 1 : 2); ++j)
+                r.s4[i][j] = __builtin_amdgcn_raw_buffer_load_b32(b, (uint32_t)(lane & 15) * (uint32_t)(K / 32),
+                                                                  (uint32_t)row[i] * (uint32_t)(K / 32) + p * 8 + j * 4, 0);
     }
+}
+
+// f(true) for the last, half piece of a row, else f(false): MXFP4 pieces hold 256
+// values, and rows a multiple of 128.
+template <class WT, class Fn>
+__device__ __forceinline__ void by_half(bool half, const Fn& f)
+{
+    if constexpr (std::is_same_v<WT, fp4_t>) {
+        if (half) {
+            f(std::true_type());
+            return;
+        }
+    }
+    f(std::false_type());
 }
 
 // Fills D - 1 buffers, then calls one(buffer, next buffer to fill) until it is false;
@@ -273,14 +330,17 @@ __device__ __forceinline__ void put(bf16_t* p, float v) { *p = f32_to_bf16(v); }
 
 // ------------------------------------------------------------------- FC1
 template <class WT>
-__global__ __launch_bounds__(kThreads, 4) void few_fc1_kernel(FewArgs a, RouteArgs ra)
+__global__ __launch_bounds__(kThreads) void few_fc1_kernel(FewArgs a, RouteArgs ra)
 {
     using F = Form<WT>;
     using act = typename F::act;
     __shared__ Tables tb;
     __shared__ union {
         RouteLds route[kWaves];
-        f32x4_t red[2][kWaves][2][64];  // [turn][wave][gate, up][lane]
+        struct {
+            f32x4_t red[2][kWaves][2][64];  // [turn][wave][gate, up][lane]
+            char stage[kWaves][Piece<WT, 2>::kStage];
+        } s;
     } lds;
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -312,15 +372,16 @@ __global__ __launch_bounds__(kThreads, 4) void few_fc1_kernel(FewArgs a, RouteAr
     // nothing).  The loads run kDepth - 1 steps ahead, across items.  Each step has its
     // registers by name (unrolled), and loads and multiplies in one branch: copied
     // registers or a join between the two would make the compiler wait for them.
-    const int tiles = a.I / 16, np = a.H / F::kPE, items = tb.nchunks * tiles;
+    const int tiles = a.I / 16, np = (a.H + F::kPE - 1) / F::kPE, items = __builtin_amdgcn_readfirstlane(tb.nchunks) * tiles;
     const int steps = (np + kWaves - 1) / kWaves;
-    const size_t stride = (size_t)a.I * F::bytes(a.H);
+    const bool ragged = a.H % F::kPE != 0;  // the last piece is half a one
+    const uint32_t ld = F::bytes(a.H), woff = (lane >> 3) * ld + (lane & 7) * 16;
+    const Buffer xb = make_buffer(a.x);
+    char* stage = lds.s.stage[wave];
     struct Loads {  // where the loads are
         int item, step, e, row[2];
-        const char* w;  // scalar
         uint32_t voff;
     } ahead;
-    const uint32_t woff = (uint32_t)(lane & 15) * (uint32_t)F::bytes(a.H) + g * 16;
     auto enter = [&](int item) {
         ahead.item = item;
         ahead.step = 0;
@@ -330,21 +391,26 @@ __global__ __launch_bounds__(kThreads, 4) void few_fc1_kernel(FewArgs a, RouteAr
         ahead.e = c.e;
         ahead.row[0] = col;
         ahead.row[1] = a.I + col;
-        ahead.w = a.w13 + ((size_t)c.e * 2 * a.I + col) * F::bytes(a.H);
         ahead.voff = (uint32_t)(token_of(a, tb, c, row) * a.H + g * (F::kPerLoad / 4)) * (uint32_t)sizeof(act);
     };
     Piece<WT, 2> buf[F::kDepth];
     auto fetch = [&](Piece<WT, 2>& r) {
         const int p = min(wave + ahead.step * kWaves, np - 1);
-        r.load(ahead.w, stride, woff, a.x, ahead.voff, p);
-        load_scales<WT, 2>(r, a.s13, ahead.e, 2 * a.I, a.H, ahead.row, p, lane);
+        by_half<WT>(ragged && p == np - 1, [&](auto half) {
+            r.template load<decltype(half)::value>(make_buffer(a.w13 + (size_t)ahead.e * 2 * a.I * ld),
+                                                   ahead.row[0] * ld + F::bytes(p * F::kPE), a.I * ld, ld, woff, xb,
+                                                   p * F::kPE * (uint32_t)sizeof(act), ahead.voff);
+            load_scales<decltype(half)::value>(r, a.s13, ahead.e, 2 * a.I, a.H, ahead.row, p, lane);
+        });
         if (++ahead.step == steps) enter(ahead.item + gridDim.x);
     };
     int item = blockIdx.x, step = 0, turn = 0;
     if (item >= items) return;
     f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
     auto multiply = [&](const Piece<WT, 2>& r) {
-        if (wave + step * kWaves < np) r.add(acc, g);
+        const int p = wave + step * kWaves;
+        if (p < np)
+            by_half<WT>(ragged && p == np - 1, [&](auto half) { r.template add<decltype(half)::value>(acc, stage, lane); });
     };
     auto one = [&](const Piece<WT, 2>& r, Piece<WT, 2>& next) {  // false after the last item
         if (ahead.item < items) {
@@ -354,12 +420,12 @@ __global__ __launch_bounds__(kThreads, 4) void few_fc1_kernel(FewArgs a, RouteAr
             multiply(r);
         }
         if (++step < steps) return true;
-        lds.red[turn][wave][0][lane] = acc[0];
-        lds.red[turn][wave][1][lane] = acc[1];
+        lds.s.red[turn][wave][0][lane] = acc[0];
+        lds.s.red[turn][wave][1][lane] = acc[1];
         acc[0] = acc[1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         lds_barrier();  // the other turn's buffer is free once every wave has come here
-        if (tid < 256) {
-            const float* sums = reinterpret_cast<const float*>(lds.red[turn]);
+        if (wave < 4) {
+            const float* sums = reinterpret_cast<const float*>(lds.s.red[turn]);
             float gt = 0.0f, up = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
@@ -383,12 +449,13 @@ __global__ __launch_bounds__(kThreads, 4) void few_fc1_kernel(FewArgs a, RouteAr
 
 // ------------------------------------------------------------------- FC2
 template <class WT>
-__global__ __launch_bounds__(kThreads, 4) void few_fc2_kernel(FewArgs a)
+__global__ __launch_bounds__(kThreads) void few_fc2_kernel(FewArgs a)
 {
     using F = Form<WT>;
     using act = typename F::act;
     __shared__ Tables tb;
     __shared__ float weight[kMaxPairs];                      // of each routed row
+    __shared__ __attribute__((aligned(16))) char stage[kWaves][Piece<WT, 1>::kStage];
     __shared__ f32x4_t ys[kWaves][MOE_FEW_MAX_T][4];         // each wave's sums: 16 columns a token
     const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -401,15 +468,15 @@ __global__ __launch_bounds__(kThreads, 4) void few_fc2_kernel(FewArgs a)
 
     // ---- column tiles.  A wave's pieces are every eighth of all (chunk, piece) pairs;
     // the loads run ahead as in FC1, within a tile.
-    const int np = a.I / F::kPE, all = tb.nchunks * np, tiles = a.H / 16;
-    const uint32_t woff = (uint32_t)(lane & 15) * (uint32_t)F::bytes(a.I) + g * 16;
+    const int np = (a.I + F::kPE - 1) / F::kPE, all = __builtin_amdgcn_readfirstlane(tb.nchunks) * np, tiles = a.H / 16;
+    const bool ragged = a.I % F::kPE != 0;
+    const uint32_t ld = F::bytes(a.I), woff = (lane >> 3) * ld + (lane & 7) * 16;
+    const Buffer hb = make_buffer(a.h);
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         for (int i = lane; i < a.T * 4; i += 64) ys[wave][i >> 2][i & 3] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         struct Loads {
             int q, chunk, p, e, row[1];
-            const char* w;  // scalar
-            const char* v;  // scalar: the chunk's first row
-            uint32_t voff;
+            uint32_t vat, voff;  // the chunk's first row; the lane's place
         } ahead;
         const int row0 = tile * 16;
         auto enter = [&](int q) {
@@ -422,26 +489,33 @@ __global__ __launch_bounds__(kThreads, 4) void few_fc2_kernel(FewArgs a)
             const Chunk c = get_chunk(a, tb, chunk);
             ahead.e = c.e;
             ahead.row[0] = row0;
-            ahead.w = a.w2 + ((size_t)c.e * a.H + row0) * F::bytes(a.I);
-            ahead.v = a.h + (size_t)c.row0 * a.I * sizeof(act);
+            ahead.vat = (uint32_t)(c.row0 * a.I) * (uint32_t)sizeof(act);
             ahead.voff = (uint32_t)(min(lane & 15, c.n - 1) * a.I + g * (F::kPerLoad / 4)) * (uint32_t)sizeof(act);
         };
         Piece<WT, 1> buf[F::kDepth];
         auto fetch = [&](Piece<WT, 1>& r) {
-            r.load(ahead.w, 0, woff, ahead.v, ahead.voff, ahead.p);
-            load_scales<WT, 1>(r, a.s2, ahead.e, a.H, a.I, ahead.row, ahead.p, lane);
+            by_half<WT>(ragged && ahead.p == np - 1, [&](auto half) {
+                r.template load<decltype(half)::value>(make_buffer(a.w2 + (size_t)ahead.e * a.H * ld),
+                                                       row0 * ld + F::bytes(ahead.p * F::kPE), 0, ld, woff, hb,
+                                                       ahead.vat + ahead.p * F::kPE * (uint32_t)sizeof(act), ahead.voff);
+                load_scales<decltype(half)::value>(r, a.s2, ahead.e, a.H, a.I, ahead.row, ahead.p, lane);
+            });
             enter(ahead.q + kWaves);
         };
         int q = wave;
         f32x4_t acc[1] = {{0.f, 0.f, 0.f, 0.f}};
         auto one = [&](const Piece<WT, 1>& r, Piece<WT, 1>& next) {
+            const int chunk = q / np;
+            auto multiply = [&] {
+                by_half<WT>(ragged && q - chunk * np == np - 1,
+                            [&](auto half) { r.template add<decltype(half)::value>(acc, stage[wave], lane); });
+            };
             if (ahead.q < all) {
                 fetch(next);
-                r.add(acc, g);
+                multiply();
             } else {
-                r.add(acc, g);
+                multiply();
             }
-            const int chunk = q / np;
             q += kWaves;
             if (q >= all || q / np != chunk) {  // the wave's last piece of this chunk: its rows to their tokens
                 const Chunk c = get_chunk(a, tb, chunk);
