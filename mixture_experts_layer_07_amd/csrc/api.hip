@@ -738,7 +738,7 @@ static moe_status check_few(int T, int H, int I, int E, int k, int n_shared, int
 
 size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int k, int n_shared, int act)
 {
-    if (check_few(T, H, I, E, k, n_shared, act, act) != MOE_OK) return 0;
+    if (check_few(T, H, I, E, k, n_shared, act, act) != MOE_OK || T == 0) return 0;
     return few_scratch_bytes(T, I, k, n_shared, act);
 }
 

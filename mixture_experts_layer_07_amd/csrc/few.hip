@@ -13,18 +13,20 @@
 //
 // A workgroup of eight waves takes 16 columns (of h: 16 gate and 16 up rows of the
 // weights) at a time; the waves share out the reduction length in pieces and add
-// their sums through LDS.  Weights go from memory to registers, the next pieces'
-// loads in flight while a piece is multiplied, 128 whole bytes of a row in eight lanes
-// (a lane's own row, 64 bytes of 16 rows a load, is what the MFMA takes, but streams
-// 4.5 TB/s where this does 6: the lanes of a wave exchange a piece through LDS of
-// their own).  The 16 rows of a column tile are the first operand of the MFMA, up
-// to 16 of the expert's tokens the second (rows past the last token repeat it: a
-// column of the result depends on its own token alone).  An expert with more
-// tokens is taken in chunks of 16.
+// their sums through LDS.  The next pieces' loads are in flight, to registers, while
+// a piece is multiplied.  A load takes 128 whole bytes of a row in eight lanes: the
+// lane's own row, 64 bytes of 16 rows a load, is what the MFMA takes, but streams
+// 4.5 TB/s where this does 6 to 7, so the lanes of a wave exchange a piece through
+// LDS of their own.  So are the activations: the CU's return path of loads is what
+// bounds the narrow weights (94% busy with MXFP4 when each lane loaded its own
+// fragments of both, 16 loads for 4 KB of weights, where now it is 5 to 8), and
+// where no expert has more than four tokens a piece of theirs is one or two loads.
+// The 16 rows of a column tile are the first operand of the MFMA, up to 16 of the
+// expert's tokens the second (rows past the last token repeat it: a column of the
+// result depends on its own token alone).  An expert with more tokens is taken in
+// chunks of 16.
 // MFMA forms: fp32 16x16x4, else bf16 16x16x32; e4m3 codes are widened to bf16 (exact)
 // and each 128-wide block's sum is scaled in fp32, MXFP4 codes with their scales (exact).
-// A lane feeds the K positions that 16 bytes of its weight row hold, and loads the
-// same positions of its token.
 #include <math.h>
 
 #include <algorithm>
@@ -42,8 +44,18 @@ struct fp4_t {};  // two e2m1 codes a byte
 
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
-constexpr int kMaxPairs = MOE_FEW_MAX_T * MOE_MAX_TOPK;                     // routed rows
-constexpr int kMaxChunks = kMaxPairs + 64 * ((MOE_FEW_MAX_T + 15) / 16);    // one expert's at most 16 rows each
+constexpr int kMaxPairs = MOE_FEW_MAX_T * MOE_MAX_TOPK;                   // routed rows
+constexpr int kMaxChunks = kMaxPairs + 64 * ((MOE_FEW_MAX_T + 15) / 16);  // one expert's at most 16 rows each
+constexpr int kFew = 4;                                                   // tokens of a chunk up to which activations are few
+
+// What FC2 has to know of the routing; FC1 leaves it in the workspace.
+struct Plan {
+    int nchunks;
+    int most;                 // rows of the largest chunk
+    int chunk[kMaxChunks];    // expert << 18 | first row << 5 | rows
+    int token[kMaxPairs];     // token of each routed row
+    float weight[kMaxPairs];  // ... and its weight
+};
 
 struct FewArgs {
     const char* x;      // [T, H]
@@ -52,50 +64,55 @@ struct FewArgs {
     const void* s13;    // block scales or null
     const void* s2;
     char* h;            // [R, I], activations' type
+    Plan* plan;
     char* y;            // [T, H]
-    int32_t* ids;       // [T, k], written by FC1, read by FC2
+    int32_t* ids;       // [T, k]
     float* scales;
     int T, H, I, E, k, n_shared;
 };
 
 // ---------------------------------------------------------------- tables
-// Which experts have tokens, and whose rows are whose.
 struct Tables {
     uint32_t mask[MOE_MAX_EXPERTS];  // tokens of each expert
     int first[MOE_MAX_EXPERTS];      // first row of each expert
-    int token[kMaxPairs];            // token of each routed row
-    int chunk[kMaxChunks];           // expert << 16 | first row
-    int nchunks;
 };
+
+__device__ __forceinline__ int pack_chunk(int e, int row, int n) { return e << 18 | row << 5 | n; }
 
 // From the masks: chunks in the experts' order, first rows.  One wave, four
 // neighbouring experts a lane; the shared experts' chunks follow.
-__device__ __forceinline__ void make_chunks(const FewArgs& a, Tables& tb, int lane)
+__device__ __forceinline__ void make_chunks(const FewArgs& a, Tables& tb, Plan& plan, int lane)
 {
-    int rows = 0, chunks = 0;
+    int rows = 0, chunks = 0, most = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int n = __popc(tb.mask[4 * lane + i]);
         rows += n;
         chunks += (n + 15) / 16;
+        most = max(most, n);
     }
     int sum = rows << 16 | chunks;
     for (int d = 1; d < 64; d <<= 1) {
         const int v = __shfl_up(sum, d, 64);
         if (lane >= d) sum += v;
     }
+    const bool many = __ballot(most > kFew) != 0;
     int row = (sum >> 16) - rows, at = (sum & 0xffff) - chunks;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int e = 4 * lane + i, n = __popc(tb.mask[e]);
         tb.first[e] = row;
-        for (int r = 0; r < n; r += 16) tb.chunk[at++] = e << 16 | (row + r);
+        for (int r = 0; r < n; r += 16) plan.chunk[at++] = pack_chunk(e, row + r, min(16, n - r));
         row += n;
     }
     const int routed = __shfl(sum & 0xffff, 63, 64), per = (a.T + 15) / 16;
     for (int i = lane; i < a.n_shared * per; i += 64)
-        tb.chunk[routed + i] = (a.E + i / per) << 16 | (a.T * a.k + (i / per) * a.T + (i % per) * 16);
-    if (lane == 0) tb.nchunks = routed + a.n_shared * per;
+        plan.chunk[routed + i] = pack_chunk(a.E + i / per, a.T * a.k + (i / per) * a.T + (i % per) * 16,
+                                            min(16, a.T - (i % per) * 16));
+    if (lane == 0) {
+        plan.nchunks = routed + a.n_shared * per;
+        plan.most = many || (a.n_shared > 0 && a.T > kFew) ? 16 : kFew;
+    }
 }
 
 // Row of token t at expert e.
@@ -104,45 +121,27 @@ __device__ __forceinline__ int row_of(const Tables& tb, int e, int t)
     return tb.first[e] + __popc(tb.mask[e] & ((1u << t) - 1u));
 }
 
-// The tables from thread i's pair (expert e0 of token i / k); every thread comes here.
-__device__ __forceinline__ void make_tables(const FewArgs& a, Tables& tb, int i, int e0)
-{
-    const int t = i / a.k;  // kThreads >= kMaxPairs
-    if (i < MOE_MAX_EXPERTS) tb.mask[i] = 0;
-    __syncthreads();
-    if (t < a.T) atomicOr(&tb.mask[e0], 1u << t);
-    __syncthreads();
-    if (i < 64) make_chunks(a, tb, i);
-    __syncthreads();
-    if (t < a.T) tb.token[row_of(tb, e0, t)] = t;
-    __syncthreads();
-}
-
-// An expert's rows [row0, row0 + n) of a chunk (scalar), and the row of a lane.
+// Rows [row0, row0 + n) of expert e (all scalar).
 struct Chunk {
     int e, row0, n;
 };
-__device__ __forceinline__ Chunk get_chunk(const FewArgs& a, const Tables& tb, int c)
+__device__ __forceinline__ Chunk get_chunk(const Plan& plan, int c)
 {
-    const int v = __builtin_amdgcn_readfirstlane(tb.chunk[c]);
-    Chunk k{v >> 16, v & 0xffff, 0};
-    const int end = k.e < a.E ? __builtin_amdgcn_readfirstlane(tb.first[k.e] + __popc(tb.mask[k.e]))
-                              : a.T * a.k + (k.e - a.E + 1) * a.T;
-    k.n = min(16, end - k.row0);
-    return k;
+    const int v = __builtin_amdgcn_readfirstlane(plan.chunk[c]);
+    return {v >> 18, (v >> 5) & 0x1fff, v & 31};
 }
-__device__ __forceinline__ int token_of(const FewArgs& a, const Tables& tb, const Chunk& c, int row)
+__device__ __forceinline__ int token_of(const FewArgs& a, const Plan& plan, const Chunk& c, int row)
 {
-    return c.e < a.E ? tb.token[row] : row - a.T * a.k - (c.e - a.E) * a.T;
+    return c.e < a.E ? plan.token[row] : row - a.T * a.k - (c.e - a.E) * a.T;
 }
 
-// ---------------------------------------------------------------- pieces
 // Memory as the buffer instructions address it: a scalar base, a scalar offset and
 // one of the lane's, so that no lane holds a pointer.
 typedef __amdgpu_buffer_rsrc_t Buffer;
-__device__ __forceinline__ Buffer make_buffer(const char* p)
+__device__ __forceinline__ Buffer make_buffer(const char* p, bool valid)  // not valid: loads are zeros, and no traffic
 {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_ptr(p)), 0, 0xffffffffu, 0x00020000);
+    const int bytes = __builtin_amdgcn_readfirstlane(valid ? -1 : 0);  // scalar, as the base
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(uniform_ptr(p)), 0, bytes, 0x00020000);
 }
 template <bool NT>  // NT: streamed past the caches
 __device__ __forceinline__ u32x4_t load16(Buffer b, uint32_t lane_offset, uint32_t offset)
@@ -150,174 +149,174 @@ __device__ __forceinline__ u32x4_t load16(Buffer b, uint32_t lane_offset, uint32
     return __builtin_amdgcn_raw_buffer_load_b128(b, lane_offset, offset, NT ? 2 : 0);
 }
 
-// One piece: PE values of K of NR weight tiles (16 rows each) and of the tokens.
+// ---------------------------------------------------------------- pieces
+// The weights' forms: K values of a piece, and of 64 bytes of a row; pieces in
+// registers (one multiplied, the others on their way) with few and with many tokens
+// a chunk; whether a row may end after half a piece.
 template <class WT> struct Form;
 template <> struct Form<float> {
     using act = float;
-    static constexpr int kPE = 64, kPerLoad = 16;  // K values of a piece, and of 64 bytes of a row
-    static constexpr int kDepth = 2;               // pieces in registers: one multiplied, the others on their way
+    static constexpr int kPE = 64, kPer64 = 16, kDepthFew = 2, kDepthMany = 2;
+    static constexpr bool kHalves = false;
     static constexpr int bytes(int n) { return n * 4; }
 };
 template <> struct Form<bf16_t> {
     using act = bf16_t;
-    static constexpr int kPE = 128, kPerLoad = 32;
-    static constexpr int kDepth = 2;
+    static constexpr int kPE = 128, kPer64 = 32, kDepthFew = 2, kDepthMany = 2;
+    static constexpr bool kHalves = false;
     static constexpr int bytes(int n) { return n * 2; }
 };
 template <> struct Form<fp8_t> {
     using act = bf16_t;
-    static constexpr int kPE = 128, kPerLoad = 64;
-    static constexpr int kDepth = 3;
+    static constexpr int kPE = 128, kPer64 = 64, kDepthFew = 3, kDepthMany = 3;
+    static constexpr bool kHalves = false;
     static constexpr int bytes(int n) { return n; }
 };
 template <> struct Form<fp4_t> {
     using act = bf16_t;
-    static constexpr int kPE = 256, kPerLoad = 128;
-    static constexpr int kDepth = 2;
+    static constexpr int kPE = 256, kPer64 = 128, kDepthFew = 3, kDepthMany = 2;
+    static constexpr bool kHalves = true;
     static constexpr int bytes(int n) { return n / 2; }
 };
 
-template <class WT, int NR>
+// One piece: kPE values of K of NR weight tiles (16 rows each) and of the chunk's
+// tokens, of which there are at most kFew or 16.
+template <class WT, int NR, bool MANY>
 struct Piece {
     using F = Form<WT>;
     using act = typename F::act;
-    static constexpr int RB = F::bytes(F::kPE);                     // bytes of a row
-    static constexpr int WL = RB / 64;                              // weight fragments of a tile
-    static constexpr int PL = F::kPerLoad / 4 * (int)sizeof(act) / 16;  // activation fragments for each of them
-    static constexpr int kStage = NR * 16 * RB;                     // LDS bytes of the exchange
+    static constexpr bool kFp4 = std::is_same_v<WT, fp4_t>;
+    static constexpr int RB = F::bytes(F::kPE);                     // bytes of a weight row
+    static constexpr int WL = RB / 64;                              // weight loads, and fragments, of a tile
+    static constexpr int VB = F::kPE * (int)sizeof(act);            // bytes of a token
+    static constexpr int VT = 1024 / VB;                            // tokens of a load
+    static constexpr int VL = (MANY ? 16 : kFew) / VT;              // loads of the tokens
+    static constexpr int PL = VB / 64 / WL;                         // activation fragments for a weight fragment
+    static constexpr int kWStage = 16 * RB;                         // LDS of the exchange: a tile at a time,
+    static constexpr int kStage = kWStage + VL * 1024 + (kFp4 ? 256 : 0);  // the tokens, the scales
     u32x4_t w[NR][WL];  // load j: rows 8 (j % 2) + lane / 8, bytes 128 (j / 2) + 16 (lane % 8)
-    u32x4_t v[WL][PL];
-    float s[NR];            // fp8: the block's scale
-    uint32_t s4[NR][2];     // MXFP4: the eight scale bytes of the lane's row
+    u32x4_t v[VL];      // load i: token i VT + lane / (64 / VT), 16-byte chunk lane % (64 / VT)
+    float s[NR];        // fp8: the block's scale
+    uint32_t s4;        // MXFP4: four scale bytes of tile lane / 32, row lane / 2 % 16
+
+    // The lane's token of load i and its bytes of it.
+    static __device__ __forceinline__ int token(int lane, int i) { return i * VT + lane / (64 / VT); }
+    static __device__ __forceinline__ int chunk16(int lane) { return lane % (64 / VT) * 16; }
 
     // The piece at scalar byte offset `wat` of an expert's weights (tile i `stride`
     // bytes on, rows ld bytes apart) and `vat` of the activations, with the lane's
-    // offsets in both.  HALF: the row ends after half of the piece (MXFP4); the
-    // weights and activations of the first half stand in for the other one.
-    template <bool HALF>
+    // offsets in both.  half: the row ends after half of the piece (MXFP4); the
+    // first half stands in for the other one.
     __device__ __forceinline__ void load(Buffer wb, uint32_t wat, uint32_t stride, uint32_t ld, uint32_t woff, Buffer vb,
-                                         uint32_t vat, uint32_t voff)
+                                         uint32_t vat, const uint32_t (&voff)[VL], bool half)
     {
-        const uint32_t back = HALF && (threadIdx.x & 4) ? RB / 2 : 0;  // lanes of the second 64 bytes
+        wat = __builtin_amdgcn_readfirstlane(wat);
+        vat = __builtin_amdgcn_readfirstlane(vat);
+        uint32_t vback = 0;
+        if constexpr (F::kHalves) {
+            woff -= half && (threadIdx.x & 4) ? RB / 2 : 0;
+            vback = half && (threadIdx.x & (32 / VT)) ? VB / 2 : 0;
+        }
 #pragma unroll
         for (int i = 0; i < NR; ++i)
 #pragma unroll
             for (int j = 0; j < WL; ++j)
-                w[i][j] = load16<true>(wb, woff - back + (j >> 1) * 128, wat + i * stride + (j & 1) * 8 * ld);
+                w[i][j] = load16<true>(wb, woff + (j >> 1) * 128, wat + i * stride + (j & 1) * 8 * ld);
 #pragma unroll
-        for (int j = 0; j < WL; ++j)
-#pragma unroll
-            for (int i = 0; i < PL; ++i)
-                v[j][i] = load16<false>(vb, voff + (HALF ? 0 : j) * F::kPerLoad * (int)sizeof(act) + i * 16, vat);
+        for (int i = 0; i < VL; ++i) v[i] = load16<false>(vb, voff[i] - vback, vat);
     }
 
-    // Lane l's rows become fragments: tile row l % 16, chunk 4 (j % 2) + l / 16 of 128 bytes.
-    __device__ __forceinline__ void exchange(char* stage, int lane, u32x4_t (&f)[NR][WL]) const
+    // The scales of piece p of tiles whose first rows are row[] of an expert's N.
+    __device__ __forceinline__ void load_scales(const void* scale, int e, int N, int K, const int (&row)[NR], int p, int lane,
+                                                bool half, bool valid)
     {
+        if constexpr (std::is_same_v<WT, fp8_t>) {
+            const __attribute__((address_space(4))) float* sp = (const __attribute__((address_space(4))) float*)scale;
 #pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-            for (int j = 0; j < WL; ++j)
-                *reinterpret_cast<u32x4_t*>(stage + (i * (WL / 2) + (j >> 1)) * 2048 +
-                                            dma_off((j & 1) * 8 + (lane >> 3), lane & 7)) = w[i][j];
-        wave_lds_fence();
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-            for (int j = 0; j < WL; ++j)
-                f[i][j] = *reinterpret_cast<const u32x4_t*>(stage + (i * (WL / 2) + (j >> 1)) * 2048 +
-                                                            dma_off(lane & 15, (j & 1) * 4 + (lane >> 4)));
+            for (int i = 0; i < NR; ++i) s[i] = sp[((size_t)e * (N / 128) + row[i] / 128) * (K / 128) + p];
+        } else if constexpr (kFp4) {
+            const Buffer b = make_buffer(static_cast<const char*>(scale) + (size_t)e * N * (K / 32), valid);
+            const uint32_t r = row[NR == 2 && lane >= 32 ? NR - 1 : 0] + (lane >> 1) % 16;
+            s4 = __builtin_amdgcn_raw_buffer_load_b32(b, r * (uint32_t)(K / 32) + (half ? 0 : (lane & 1) * 4),
+                                                      __builtin_amdgcn_readfirstlane(p * 8), 0);
+        }
     }
 
-    // HALF: of the second half nothing.
-    template <bool HALF>
-    __device__ __forceinline__ void add(f32x4_t (&acc)[NR], char* stage, int lane) const
+    // acc += the piece's product with the chunk's n tokens, through the wave's own
+    // `stage`.  Row l % 16 of a tile and token l % 16 (the last one's past it) are
+    // lane l's, with 16-byte chunk 4 (j % 2) + l / 16 of each 128 bytes of the weights.
+    __device__ __forceinline__ void add(f32x4_t (&acc)[NR], char* stage, int lane, int n, bool half) const
     {
-        u32x4_t f[NR][WL];
-        exchange(stage, lane, f);
-        constexpr int N = HALF ? WL / 2 : WL;
-        if constexpr (std::is_same_v<WT, float>) {
+        const int r = lane & 15, g = lane >> 4;
+        char* vs = stage + kWStage;
 #pragma unroll
-            for (int j = 0; j < N; ++j)
+        for (int i = 0; i < VL; ++i) {
+            const int c = chunk16(lane);
+            *reinterpret_cast<u32x4_t*>(vs + (c >> 7) * (VL * VT * 128) + dma_off(token(lane, i), (c >> 4) & 7)) = v[i];
+        }
+        if constexpr (kFp4) *reinterpret_cast<uint32_t*>(vs + VL * 1024 + lane * 4) = s4;
+        u32x4_t a[WL][PL];
+        const int t = min(r, n - 1);
 #pragma unroll
-                for (int i = 0; i < NR; ++i)
+        for (int i = 0; i < NR; ++i) {
+            u32x4_t f[WL];
+#pragma unroll
+            for (int j = 0; j < WL; ++j)
+                *reinterpret_cast<u32x4_t*>(stage + (j >> 1) * 2048 + dma_off((j & 1) * 8 + (lane >> 3), lane & 7)) = w[i][j];
+            wave_lds_fence();
+            if (i == 0) {
+#pragma unroll
+                for (int j = 0; j < WL; ++j)
+#pragma unroll
+                    for (int q = 0; q < PL; ++q) {
+                        const int c = (j * 4 + g) * PL + q;  // of the token's 16-byte chunks
+                        a[j][q] = *reinterpret_cast<const u32x4_t*>(vs + (c >> 3) * (VL * VT * 128) + dma_off(t, c & 7));
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < WL; ++j)
+                f[j] = *reinterpret_cast<const u32x4_t*>(stage + (j >> 1) * 2048 + dma_off(r, (j & 1) * 4 + g));
+            if constexpr (std::is_same_v<WT, float>) {
+#pragma unroll
+                for (int j = 0; j < WL; ++j)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
-                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(f[i][j][c]), __uint_as_float(v[j][0][c]),
+                        acc[i] = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(f[j][c]), __uint_as_float(a[j][0][c]),
                                                                       acc[i], 0, 0, 0);
-        } else if constexpr (std::is_same_v<WT, bf16_t>) {
+            } else if constexpr (std::is_same_v<WT, bf16_t>) {
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-#pragma unroll
-                for (int i = 0; i < NR; ++i) acc[i] = mfma_frag(f[i][j], v[j][0], acc[i], bf16_t());
-        } else if constexpr (std::is_same_v<WT, fp8_t>) {
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
+                for (int j = 0; j < WL; ++j) acc[i] = mfma_frag(f[j], a[j][0], acc[i], bf16_t());
+            } else if constexpr (std::is_same_v<WT, fp8_t>) {
                 f32x4_t part = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    part = mfma_frag(fp8x8_to_bf16x8(f[i][j].x, f[i][j].y), v[j][0], part, bf16_t());
-                    part = mfma_frag(fp8x8_to_bf16x8(f[i][j].z, f[i][j].w), v[j][1], part, bf16_t());
+                for (int j = 0; j < WL; ++j) {
+                    part = mfma_frag(fp8x8_to_bf16x8(f[j].x, f[j].y), a[j][0], part, bf16_t());
+                    part = mfma_frag(fp8x8_to_bf16x8(f[j].z, f[j].w), a[j][1], part, bf16_t());
                 }
                 acc[i] += s[i] * part;
-            }
-        } else {
+            } else {
+                typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+                const u32x2_t sc = *reinterpret_cast<const u32x2_t*>(vs + VL * 1024 + (i * 16 + r) * 8);
 #pragma unroll
-            for (int j = 0; j < N; ++j)
-#pragma unroll
-                for (int i = 0; i < NR; ++i) {
-                    const uint32_t sc = (s4[i][j] >> (8 * (lane >> 4))) & 0xffu;
+                for (int j = 0; j < WL; ++j) {
+                    if (j > 0 && half) break;
+                    const uint32_t byte = (sc[j] >> (8 * g)) & 0xffu;
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
-                        acc[i] = mfma_frag(mxfp4_to_bf16x8(f[i][j][q], sc), v[j][q], acc[i], bf16_t());
+                        acc[i] = mfma_frag(mxfp4_to_bf16x8(f[j][q], byte), a[j][q], acc[i], bf16_t());
                 }
+            }
         }
     }
 };
 
-// The scales of piece p of NR tiles whose first rows are row[]: fp8, one value a tile
-// (scalar); MXFP4, eight bytes of the lane's row (HALF: four).
-template <bool HALF, class WT, int NR>
-__device__ __forceinline__ void load_scales(Piece<WT, NR>& r, const void* scale, int e, int N, int K, const int (&row)[NR],
-                                            int p, int lane)
-{
-    if constexpr (std::is_same_v<WT, fp8_t>) {
-        const __attribute__((address_space(4))) float* s = (const __attribute__((address_space(4))) float*)scale;
-#pragma unroll
-        for (int i = 0; i < NR; ++i) r.s[i] = s[((size_t)e * (N / 128) + row[i] / 128) * (K / 128) + p];
-    } else if constexpr (std::is_same_v<WT, fp4_t>) {
-        const Buffer b = make_buffer(static_cast<const char*>(scale) + (size_t)e * N * (K / 32));
-#pragma unroll
-        for (int i = 0; i < NR; ++i)
-#pragma unroll
-            for (int j = 0; j < (HALF ? 1 : 2); ++j)
-                r.s4[i][j] = __builtin_amdgcn_raw_buffer_load_b32(b, (uint32_t)(lane & 15) * (uint32_t)(K / 32),
-                                                                  (uint32_t)row[i] * (uint32_t)(K / 32) + p * 8 + j * 4, 0);
-    }
-}
-
-// f(true) for the last, half piece of a row, else f(false): MXFP4 pieces hold 256
-// values, and rows a multiple of 128.
-template <class WT, class Fn>
-__device__ __forceinline__ void by_half(bool half, const Fn& f)
-{
-    if constexpr (std::is_same_v<WT, fp4_t>) {
-        if (half) {
-            f(std::true_type());
-            return;
-        }
-    }
-    f(std::false_type());
-}
-
 // Fills D - 1 buffers, then calls one(buffer, next buffer to fill) until it is false;
 // unrolled, so that every buffer is a set of registers.
-template <int D, class P, class Fetch, class One, class More>
-__device__ __forceinline__ void run_pipeline(P (&buf)[D], Fetch& fetch, One& one, const More& more)
+template <int D, class P, class Fetch, class One>
+__device__ __forceinline__ void run_pipeline(P (&buf)[D], Fetch& fetch, One& one)
 {
 #pragma unroll
-    for (int i = 0; i < D - 1; ++i)
-        if (more()) fetch(buf[i]);
+    for (int i = 0; i < D - 1; ++i) fetch(buf[i]);
     while (true) {
 #pragma unroll
         for (int i = 0; i < D; ++i)
@@ -329,111 +328,76 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(bf16_t* p, float v) { *p = f32_to_bf16(v); }
 
 // ------------------------------------------------------------------- FC1
-template <class WT>
-__global__ __launch_bounds__(kThreads) void few_fc1_kernel(FewArgs a, RouteArgs ra)
+typedef f32x4_t Sums[2][kWaves][2][64];  // [turn][wave][gate, up][lane]
+
+// The (chunk, column tile) items of this workgroup.  Piece p of an item is wave
+// p % 8's; every wave takes the same number of steps (past the end it loads and adds
+// nothing).  The loads run D - 1 steps ahead, across items, and go on past the last
+// one with an empty buffer: each step has its registers by name (unrolled) and its
+// loads under no condition, where copied registers or a join of two branches would
+// make the compiler wait for them.
+template <class WT, bool MANY>
+__device__ __forceinline__ void fc1_items(const FewArgs& a, const Plan& plan, Sums& red, char* stage, int wave, int lane)
 {
     using F = Form<WT>;
     using act = typename F::act;
-    __shared__ Tables tb;
-    __shared__ union {
-        RouteLds route[kWaves];
-        struct {
-            f32x4_t red[2][kWaves][2][64];  // [turn][wave][gate, up][lane]
-            char stage[kWaves][Piece<WT, 2>::kStage];
-        } s;
-    } lds;
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
-    // ---- routing of every token, by every workgroup; the first one writes it out
-    __shared__ int ids[kMaxPairs];
-#pragma unroll 1
-    for (int t = wave; t < a.T; t += kWaves) {
-        int id[MOE_MAX_TOPK];
-        float scale[MOE_MAX_TOPK];
-        const bool first = blockIdx.x == 0;
-        if (first) route_token<true>(ra, t, lane, lds.route[wave], id, scale);
-        else route_token<false>(ra, t, lane, lds.route[wave], id, scale);
-#pragma unroll
-        for (int j = 0; j < MOE_MAX_TOPK; ++j)
-            if (j < a.k && lane == j) {
-                ids[t * a.k + j] = id[j];
-                if (first) {
-                    a.ids[t * a.k + j] = id[j];
-                    a.scales[t * a.k + j] = scale[j];
-                }
-            }
-    }
-    __syncthreads();
-    make_tables(a, tb, tid, tid < a.T * a.k ? ids[tid] : 0);
-
-    // ---- (chunk, column tile) items.  Piece p of an item is wave p % 8's; every wave
-    // takes the same number of steps (past the end it loads the last piece and adds
-    // nothing).  The loads run kDepth - 1 steps ahead, across items.  Each step has its
-    // registers by name (unrolled), and loads and multiplies in one branch: copied
-    // registers or a join between the two would make the compiler wait for them.
-    const int tiles = a.I / 16, np = (a.H + F::kPE - 1) / F::kPE, items = __builtin_amdgcn_readfirstlane(tb.nchunks) * tiles;
+    using P = Piece<WT, 2, MANY>;
+    const int tiles = a.I / 16, np = (a.H + F::kPE - 1) / F::kPE;
+    const int items = __builtin_amdgcn_readfirstlane(plan.nchunks) * tiles;
     const int steps = (np + kWaves - 1) / kWaves;
     const bool ragged = a.H % F::kPE != 0;  // the last piece is half a one
     const uint32_t ld = F::bytes(a.H), woff = (lane >> 3) * ld + (lane & 7) * 16;
-    const Buffer xb = make_buffer(a.x);
-    char* stage = lds.s.stage[wave];
     struct Loads {  // where the loads are
         int item, step, e, row[2];
-        uint32_t voff;
+        uint32_t voff[P::VL];
+        bool valid;
     } ahead;
     auto enter = [&](int item) {
         ahead.item = item;
         ahead.step = 0;
-        if (item >= items) return;
-        const Chunk c = get_chunk(a, tb, item / tiles);
-        const int col = item % tiles * 16, row = c.row0 + min(lane & 15, c.n - 1);
+        ahead.valid = item < items;
+        if (!ahead.valid) return;
+        const Chunk c = get_chunk(plan, item / tiles);
         ahead.e = c.e;
-        ahead.row[0] = col;
-        ahead.row[1] = a.I + col;
-        ahead.voff = (uint32_t)(token_of(a, tb, c, row) * a.H + g * (F::kPerLoad / 4)) * (uint32_t)sizeof(act);
+        ahead.row[0] = item % tiles * 16;
+        ahead.row[1] = a.I + ahead.row[0];
+#pragma unroll
+        for (int i = 0; i < P::VL; ++i) {
+            const int row = c.row0 + min(P::token(lane, i), c.n - 1);
+            ahead.voff[i] = (uint32_t)(token_of(a, plan, c, row) * a.H) * (uint32_t)sizeof(act) + P::chunk16(lane);
+        }
     };
-    Piece<WT, 2> buf[F::kDepth];
-    auto fetch = [&](Piece<WT, 2>& r) {
+    P buf[MANY ? F::kDepthMany : F::kDepthFew];
+    auto fetch = [&](P& r) {
         const int p = min(wave + ahead.step * kWaves, np - 1);
-        by_half<WT>(ragged && p == np - 1, [&](auto half) {
-            r.template load<decltype(half)::value>(make_buffer(a.w13 + (size_t)ahead.e * 2 * a.I * ld),
-                                                   ahead.row[0] * ld + F::bytes(p * F::kPE), a.I * ld, ld, woff, xb,
-                                                   p * F::kPE * (uint32_t)sizeof(act), ahead.voff);
-            load_scales<decltype(half)::value>(r, a.s13, ahead.e, 2 * a.I, a.H, ahead.row, p, lane);
-        });
+        const bool valid = ahead.valid && wave + ahead.step * kWaves < np, half = F::kHalves && ragged && p == np - 1;
+        r.load(make_buffer(a.w13 + (size_t)ahead.e * 2 * a.I * ld, valid), ahead.row[0] * ld + F::bytes(p * F::kPE),
+               a.I * ld, ld, woff, make_buffer(a.x, valid), p * P::VB, ahead.voff, half);
+        r.load_scales(a.s13, ahead.e, 2 * a.I, a.H, ahead.row, p, lane, half, valid);
         if (++ahead.step == steps) enter(ahead.item + gridDim.x);
     };
     int item = blockIdx.x, step = 0, turn = 0;
     if (item >= items) return;
+    Chunk c = get_chunk(plan, item / tiles);
     f32x4_t acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    auto multiply = [&](const Piece<WT, 2>& r) {
+    auto one = [&](const P& r, P& next) {  // false after the last item
+        fetch(next);
         const int p = wave + step * kWaves;
-        if (p < np)
-            by_half<WT>(ragged && p == np - 1, [&](auto half) { r.template add<decltype(half)::value>(acc, stage, lane); });
-    };
-    auto one = [&](const Piece<WT, 2>& r, Piece<WT, 2>& next) {  // false after the last item
-        if (ahead.item < items) {
-            fetch(next);
-            multiply(r);
-        } else {
-            multiply(r);
-        }
+        if (p < np) r.add(acc, stage, lane, c.n, F::kHalves && ragged && p == np - 1);
         if (++step < steps) return true;
-        lds.s.red[turn][wave][0][lane] = acc[0];
-        lds.s.red[turn][wave][1][lane] = acc[1];
+        red[turn][wave][0][lane] = acc[0];
+        red[turn][wave][1][lane] = acc[1];
         acc[0] = acc[1] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         lds_barrier();  // the other turn's buffer is free once every wave has come here
         if (wave < 4) {
-            const float* sums = reinterpret_cast<const float*>(lds.s.red[turn]);
+            const int i = wave * 64 + lane, n = (i >> 2) & 15, col = item % tiles * 16 + (i >> 6) * 4 + (i & 3);
+            const float* sums = reinterpret_cast<const float*>(red[turn]);
             float gt = 0.0f, up = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                gt += sums[w * 512 + tid];
-                up += sums[w * 512 + 256 + tid];
+                gt += sums[w * 512 + i];
+                up += sums[w * 512 + 256 + i];
             }
-            const Chunk c = get_chunk(a, tb, item / tiles);
-            const int n = (tid >> 2) & 15, col = item % tiles * 16 + (tid >> 6) * 4 + (tid & 3);
             if (n < c.n)
                 put(reinterpret_cast<act*>(a.h) + (size_t)(c.row0 + n) * a.I + col,
                     gt * __builtin_amdgcn_rcpf(1.0f + expf(-gt)) * up);
@@ -441,119 +405,207 @@ __global__ __launch_bounds__(kThreads) void few_fc1_kernel(FewArgs a, RouteArgs 
         turn ^= 1;
         step = 0;
         item += gridDim.x;
-        return item < items;
+        if (item >= items) return false;
+        c = get_chunk(plan, item / tiles);
+        return true;
     };
     enter(item);
-    run_pipeline<F::kDepth>(buf, fetch, one, [&] { return ahead.item < items; });
+    run_pipeline(buf, fetch, one);
+}
+
+// MAYBE: an expert may have more than kFew tokens (a call of at most kFew has a
+// kernel of its own, whose smaller stage leaves room for a second workgroup).
+template <class WT, bool MAYBE>
+__global__ __launch_bounds__(kThreads) void few_fc1_kernel(FewArgs a, RouteArgs ra)
+{
+    constexpr int kStage = Piece<WT, 2, MAYBE>::kStage;
+    __shared__ Tables tb;
+    __shared__ Plan plan;
+    __shared__ __attribute__((aligned(16))) union {
+        RouteLds route[kWaves];
+        struct {
+            Sums red;
+            char stage[kWaves][kStage];
+        } s;
+    } lds;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+
+    // ---- routing of every token, by every workgroup; the last one, which has the
+    // fewest items, writes it out
+    const bool last = blockIdx.x == gridDim.x - 1;
+    __shared__ int ids[kMaxPairs];
+    float logit[4], scale = 0.0f;
+    if (wave < a.T) load_logits(ra, wave, lane, logit);
+    if (tid < MOE_MAX_EXPERTS) tb.mask[tid] = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int t = wave; t < a.T; t += kWaves) {
+        float more[4];
+        if (t + kWaves < a.T) load_logits(ra, t + kWaves, lane, more);
+        int id;
+        if (last) route_token<true>(ra, logit, lane, lds.route[wave], id, scale);
+        else route_token<false>(ra, logit, lane, lds.route[wave], id, scale);
+        if (lane < a.k) {
+            ids[t * a.k + lane] = id;
+            atomicOr(&tb.mask[id], 1u << t);
+            if (last) {
+                a.ids[t * a.k + lane] = id;
+                a.scales[t * a.k + lane] = scale;
+                plan.weight[t * a.k + lane] = scale;  // by pair until the rows are known
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) logit[i] = more[i];
+    }
+    __syncthreads();
+    if (wave == 0) make_chunks(a, tb, plan, lane);
+    __syncthreads();
+    const int pairs = a.T * a.k;  // kThreads >= kMaxPairs
+    int row = 0;
+    if (tid < pairs) {
+        row = row_of(tb, ids[tid], tid / a.k);
+        plan.token[row] = tid / a.k;
+        if (last) {
+            a.plan->token[row] = tid / a.k;
+            a.plan->weight[row] = plan.weight[tid];
+        }
+    }
+    __syncthreads();
+    if (last) {
+        for (int i = tid; i < plan.nchunks; i += kThreads) a.plan->chunk[i] = plan.chunk[i];
+        if (tid == 0) {
+            a.plan->nchunks = plan.nchunks;
+            a.plan->most = plan.most;
+        }
+    }
+    if (!MAYBE || __builtin_amdgcn_readfirstlane(plan.most) <= kFew)
+        fc1_items<WT, false>(a, plan, lds.s.red, lds.s.stage[wave], wave, lane);
+    else
+        fc1_items<WT, MAYBE>(a, plan, lds.s.red, lds.s.stage[wave], wave, lane);
 }
 
 // ------------------------------------------------------------------- FC2
-template <class WT>
-__global__ __launch_bounds__(kThreads) void few_fc2_kernel(FewArgs a)
+typedef f32x4_t Columns[kWaves][MOE_FEW_MAX_T][4];  // each wave's sums: 16 columns a token
+
+// The column tiles of this workgroup.  A wave's pieces are every eighth of all
+// (chunk, piece) pairs; the loads run ahead as in FC1, within a tile.
+template <class WT, bool MANY>
+__device__ __forceinline__ void fc2_tiles(const FewArgs& a, const Plan& plan, Columns& ys, char* stage, int wave, int lane)
 {
     using F = Form<WT>;
     using act = typename F::act;
-    __shared__ Tables tb;
-    __shared__ float weight[kMaxPairs];                      // of each routed row
-    __shared__ __attribute__((aligned(16))) char stage[kWaves][Piece<WT, 1>::kStage];
-    __shared__ f32x4_t ys[kWaves][MOE_FEW_MAX_T][4];         // each wave's sums: 16 columns a token
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-
-    // ---- the tables again, from the ids
-    const int pairs = a.T * a.k, e0 = tid < pairs ? a.ids[tid] : 0;
-    make_tables(a, tb, tid, e0);
-    if (tid < pairs) weight[row_of(tb, e0, tid / a.k)] = a.scales[tid];
-    __syncthreads();
-
-    // ---- column tiles.  A wave's pieces are every eighth of all (chunk, piece) pairs;
-    // the loads run ahead as in FC1, within a tile.
-    const int np = (a.I + F::kPE - 1) / F::kPE, all = __builtin_amdgcn_readfirstlane(tb.nchunks) * np, tiles = a.H / 16;
+    using P = Piece<WT, 1, MANY>;
+    const int np = (a.I + F::kPE - 1) / F::kPE, all = __builtin_amdgcn_readfirstlane(plan.nchunks) * np, tiles = a.H / 16;
     const bool ragged = a.I % F::kPE != 0;
     const uint32_t ld = F::bytes(a.I), woff = (lane >> 3) * ld + (lane & 7) * 16;
-    const Buffer hb = make_buffer(a.h);
+    const int g = lane >> 4;
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
         for (int i = lane; i < a.T * 4; i += 64) ys[wave][i >> 2][i & 3] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         struct Loads {
-            int q, chunk, p, e, row[1];
-            uint32_t vat, voff;  // the chunk's first row; the lane's place
+            int chunk, p, e, row[1];
+            uint32_t vat, voff[P::VL];
+            bool valid;
         } ahead;
-        const int row0 = tile * 16;
-        auto enter = [&](int q) {
-            ahead.q = q;
-            if (q >= all) return;
-            const int chunk = q / np;
-            ahead.p = q - chunk * np;
-            if (chunk == ahead.chunk) return;
+        ahead.row[0] = tile * 16;
+        auto enter = [&](int chunk) {
+            ahead.valid = chunk * np + ahead.p < all;
+            if (!ahead.valid) return;
+            const Chunk c = get_chunk(plan, chunk);
             ahead.chunk = chunk;
-            const Chunk c = get_chunk(a, tb, chunk);
             ahead.e = c.e;
-            ahead.row[0] = row0;
             ahead.vat = (uint32_t)(c.row0 * a.I) * (uint32_t)sizeof(act);
-            ahead.voff = (uint32_t)(min(lane & 15, c.n - 1) * a.I + g * (F::kPerLoad / 4)) * (uint32_t)sizeof(act);
+#pragma unroll
+            for (int i = 0; i < P::VL; ++i)
+                ahead.voff[i] = (uint32_t)(min(P::token(lane, i), c.n - 1) * a.I) * (uint32_t)sizeof(act) + P::chunk16(lane);
         };
-        Piece<WT, 1> buf[F::kDepth];
-        auto fetch = [&](Piece<WT, 1>& r) {
-            by_half<WT>(ragged && ahead.p == np - 1, [&](auto half) {
-                r.template load<decltype(half)::value>(make_buffer(a.w2 + (size_t)ahead.e * a.H * ld),
-                                                       row0 * ld + F::bytes(ahead.p * F::kPE), 0, ld, woff, hb,
-                                                       ahead.vat + ahead.p * F::kPE * (uint32_t)sizeof(act), ahead.voff);
-                load_scales<decltype(half)::value>(r, a.s2, ahead.e, a.H, a.I, ahead.row, ahead.p, lane);
-            });
-            enter(ahead.q + kWaves);
-        };
-        int q = wave;
-        f32x4_t acc[1] = {{0.f, 0.f, 0.f, 0.f}};
-        auto one = [&](const Piece<WT, 1>& r, Piece<WT, 1>& next) {
-            const int chunk = q / np;
-            auto multiply = [&] {
-                by_half<WT>(ragged && q - chunk * np == np - 1,
-                            [&](auto half) { r.template add<decltype(half)::value>(acc, stage[wave], lane); });
-            };
-            if (ahead.q < all) {
-                fetch(next);
-                multiply();
-            } else {
-                multiply();
+        P buf[MANY ? F::kDepthMany : F::kDepthFew];
+        auto fetch = [&](P& r) {
+            const bool half = F::kHalves && ragged && ahead.p == np - 1;
+            r.load(make_buffer(a.w2 + (size_t)ahead.e * a.H * ld, ahead.valid), ahead.row[0] * ld + F::bytes(ahead.p * F::kPE),
+                   0, ld, woff, make_buffer(a.h, ahead.valid), ahead.vat + ahead.p * P::VB, ahead.voff, half);
+            r.load_scales(a.s2, ahead.e, a.H, a.I, ahead.row, ahead.p, lane, half, ahead.valid);
+            if (!ahead.valid) return;
+            int chunk = ahead.chunk;
+            ahead.p += kWaves;
+            while (ahead.p >= np) {
+                ahead.p -= np;
+                ++chunk;
             }
-            q += kWaves;
-            if (q >= all || q / np != chunk) {  // the wave's last piece of this chunk: its rows to their tokens
-                const Chunk c = get_chunk(a, tb, chunk);
+            if (chunk != ahead.chunk) enter(chunk);
+        };
+        int chunk = wave / np, p = wave - chunk * np, q = wave;
+        f32x4_t acc[1] = {{0.f, 0.f, 0.f, 0.f}};
+        if (q < all) {
+            Chunk c = get_chunk(plan, chunk);
+            auto one = [&](const P& r, P& next) {
+                fetch(next);
+                r.add(acc, stage, lane, c.n, F::kHalves && ragged && p == np - 1);
+                q += kWaves;
+                p += kWaves;
+                if (p < np && q < all) return true;
+                // the wave's last piece of this chunk: its rows to their tokens
                 const int n = lane & 15, row = c.row0 + n;
                 if (n < c.n) {
-                    const float w = c.e < a.E ? weight[row] : 1.0f;
-                    ys[wave][token_of(a, tb, c, row)][g] += w * acc[0];  // the wave's own; a token is in a chunk once
+                    const float w = c.e < a.E ? plan.weight[row] : 1.0f;
+                    ys[wave][token_of(a, plan, c, row)][g] += w * acc[0];  // the wave's own; a token is in a chunk once
                 }
                 acc[0] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            }
-            return q < all;
-        };
-        ahead.chunk = -1;
-        enter(q);
-        if (q < all) run_pipeline<F::kDepth>(buf, fetch, one, [&] { return ahead.q < all; });
+                if (q >= all) return false;
+                while (p >= np) {
+                    p -= np;
+                    ++chunk;
+                }
+                c = get_chunk(plan, chunk);
+                return true;
+            };
+            ahead.p = p;
+            enter(chunk);
+            run_pipeline(buf, fetch, one);
+        }
         __syncthreads();
-        for (int i = tid; i < a.T * 16; i += kThreads) {
-            const int t = i >> 4, c = i & 15;
+        for (int i = wave * 64 + lane; i < a.T * 16; i += kThreads) {
+            const int t = i >> 4, col = i & 15;
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w) v += reinterpret_cast<const float*>(&ys[w][t][0])[c];
-            put(reinterpret_cast<act*>(a.y) + (size_t)t * a.H + row0 + c, v);
+            for (int w = 0; w < kWaves; ++w) v += reinterpret_cast<const float*>(&ys[w][t][0])[col];
+            put(reinterpret_cast<act*>(a.y) + (size_t)t * a.H + tile * 16 + col, v);
         }
         __syncthreads();
     }
 }
 
-template <class WT>
+template <class WT, bool MAYBE>
+__global__ __launch_bounds__(kThreads) void few_fc2_kernel(FewArgs a)
+{
+    constexpr int kStage = Piece<WT, 1, MAYBE>::kStage;
+    __shared__ Plan plan;
+    __shared__ __attribute__((aligned(16))) char stage[kWaves][kStage];
+    __shared__ Columns ys;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    for (int i = tid; i < (int)(sizeof(Plan) / 4); i += kThreads)
+        reinterpret_cast<int*>(&plan)[i] = reinterpret_cast<const int*>(a.plan)[i];
+    __syncthreads();
+    if (!MAYBE || __builtin_amdgcn_readfirstlane(plan.most) <= kFew)
+        fc2_tiles<WT, false>(a, plan, ys, stage[wave], wave, lane);
+    else
+        fc2_tiles<WT, MAYBE>(a, plan, ys, stage[wave], wave, lane);
+}
+
+template <class WT, bool MAYBE>
 moe_status run_few(const FewArgs& a, const RouteArgs& ra, hipStream_t s)
 {
     static const int occ1 = [] {
         int n = 0;
-        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, few_fc1_kernel<WT>, kThreads, 0) != hipSuccess || n < 1) n = 1;
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, few_fc1_kernel<WT, MAYBE>, kThreads, 0) != hipSuccess || n < 1)
+            n = 1;
         return n;
     }();
     static const int occ2 = [] {
         int n = 0;
-        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, few_fc2_kernel<WT>, kThreads, 0) != hipSuccess || n < 1) n = 1;
+        if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, few_fc2_kernel<WT, MAYBE>, kThreads, 0) != hipSuccess || n < 1)
+            n = 1;
         return n;
     }();
     const long cus = device_cu_count(), per = (a.T + 15) / 16;
@@ -561,22 +613,34 @@ moe_status run_few(const FewArgs& a, const RouteArgs& ra, hipStream_t s)
     const long g1 = std::min(chunks * (a.I / 16), cus * occ1), g2 = std::min((long)a.H / 16, cus * occ2);
     {
         TimedLaunch tl(MOE_KID_FEW_FC1, s);
-        hipLaunchKernelGGL(few_fc1_kernel<WT>, dim3((unsigned)g1), dim3(kThreads), 0, s, a, ra);
+        hipLaunchKernelGGL((few_fc1_kernel<WT, MAYBE>), dim3((unsigned)g1), dim3(kThreads), 0, s, a, ra);
     }
     moe_status st = launch_status("few_fc1_kernel");
     if (st != MOE_OK) return st;
     {
         TimedLaunch tl(MOE_KID_FEW_FC2, s);
-        hipLaunchKernelGGL(few_fc2_kernel<WT>, dim3((unsigned)g2), dim3(kThreads), 0, s, a);
+        hipLaunchKernelGGL((few_fc2_kernel<WT, MAYBE>), dim3((unsigned)g2), dim3(kThreads), 0, s, a);
     }
     return launch_status("few_fc2_kernel");
+}
+
+template <class WT>
+moe_status run_few(const FewArgs& a, const RouteArgs& ra, hipStream_t s)
+{
+    return a.T <= kFew ? run_few<WT, false>(a, ra, s) : run_few<WT, true>(a, ra, s);
+}
+
+size_t few_h_bytes(int T, int I, int k, int n_shared, int act)
+{
+    const size_t n = (size_t)T * (k + n_shared) * I * (act == MOE_F32 ? 4 : 2);
+    return (n + 255) & ~(size_t)255;
 }
 
 }  // namespace
 
 size_t few_scratch_bytes(int T, int I, int k, int n_shared, int act)
 {
-    return (size_t)T * (k + n_shared) * I * (act == MOE_F32 ? 4 : 2);
+    return few_h_bytes(T, I, k, n_shared, act) + sizeof(Plan);
 }
 
 moe_status launch_layer_few(const void* x, const float* logits, int T, int H, int I, int E, int method, int k,
@@ -591,6 +655,7 @@ moe_status launch_layer_few(const void* x, const float* logits, int T, int H, in
     a.s13 = w13_scale;
     a.s2 = w2_scale;
     a.h = static_cast<char*>(ws);
+    a.plan = reinterpret_cast<Plan*>(a.h + few_h_bytes(T, I, k, n_shared, wdt == MOE_F32 ? MOE_F32 : MOE_BF16));
     a.y = static_cast<char*>(y);
     a.ids = ids;
     a.scales = scales;

@@ -114,10 +114,18 @@ struct RouteLds {  // one wave's
     int gsel[128];
 };
 
-// Token t's experts, in every lane, and their weights if WEIGHTS.
+// A token's logits and the bias, as the lanes own them.
+__device__ __forceinline__ void load_logits(const RouteArgs& a, int t, int lane, float (&logit)[4])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) logit[i] = lane + 64 * i < a.E ? a.logits[(size_t)t * a.E + lane + 64 * i] : 0.0f;
+}
+
+// The experts of the token with these logits: lane j < k gets the j-th and, if
+// WEIGHTS, its weight.
 template <bool WEIGHTS>
-__device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane, RouteLds& s,
-                                            int (&sel_id)[MOE_MAX_TOPK], float (&scale)[MOE_MAX_TOPK])
+__device__ __forceinline__ void route_token(const RouteArgs& a, const float (&logit)[4], int lane, RouteLds& s, int& my_id,
+                                            float& my_scale)
 {
 #pragma clang fp contract(off)
     const int E = a.E, k = a.k, method = a.method;
@@ -125,13 +133,11 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
     // sigmoid-scored methods select on fl32(sigmoid) (+ bias)
     const bool sigm = dsv3 || method == MOE_ROUTE_MINIMAX2 || method == MOE_ROUTE_SIGMOID_RENORM;
 
-    float logit[4], key[4];
+    float key[4];
     bool valid[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int e = lane + 64 * i;
-        valid[i] = e < E;
-        logit[i] = valid[i] ? a.logits[(size_t)t * E + e] : 0.0f;
+        valid[i] = lane + 64 * i < E;
         key[i] = logit[i];
     }
 
@@ -199,11 +205,10 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
 #pragma unroll
     for (int i = 0; i < 4; ++i) kb[i] = ordered_bits(key[i]);
 
-    float sel_key[MOE_MAX_TOPK];
+    uint32_t my_key = 0, first_key = 0;  // of this lane's expert, of the first one
+    my_id = 0;
 #pragma unroll
     for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-        sel_id[j] = 0;
-        sel_key[j] = 0.0f;
         if (j < k) {
             // invalid candidates enter the maximum as 0, at or below every
             // valid key, and never win a ballot
@@ -217,8 +222,11 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
                 const uint64_t b = __ballot(valid[i] && kb[i] == m);
                 if (b) e = 64 * i + __ffsll((unsigned long long)b) - 1;
             }
-            sel_id[j] = e;
-            sel_key[j] = from_ordered_bits(m);
+            if (lane == j) {
+                my_id = e;
+                my_key = m;
+            }
+            if (j == 0) first_key = m;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (64 * i + lane == e) valid[i] = false;
@@ -226,42 +234,31 @@ __device__ __forceinline__ void route_token(const RouteArgs& a, int t, int lane,
     }
 
     if constexpr (!WEIGHTS) return;
-    // weights, in fp64, rounded once
-    double w[MOE_MAX_TOPK];
-    double wsum = 0.0;
+    // weights, in fp64, rounded once; summed in the experts' order
+    double w, wsum = 0.0;
     if (sigm) {
-#pragma unroll
-        for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-            w[j] = (j < k) ? (double)s.sig[sel_id[j]] : 0.0;
-            wsum += w[j];
-        }
-        if (dsv3) wsum += 1e-20;
+        w = (double)s.sig[my_id];
     } else if (method == MOE_ROUTE_LLAMA4) {
-        // the kept logits' own sigmoids, not renormalised
-#pragma unroll
-        for (int j = 0; j < MOE_MAX_TOPK; ++j)
-            w[j] = (j < k) ? 1.0 / (1.0 + exp(-(double)sel_key[j])) : 0.0;
-        wsum = 1.0;
+        w = 1.0 / (1.0 + exp(-(double)from_ordered_bits(my_key)));  // its own sigmoid, not renormalised
     } else {
-        const double m = (double)sel_key[0];
-#pragma unroll
-        for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-            w[j] = (j < k) ? exp((double)sel_key[j] - m) : 0.0;
-            wsum += w[j];
-        }
-        const bool renorm = method != MOE_ROUTE_DEFAULT || (a.flags & MOE_ROUTE_FLAG_RENORMALIZE);
-        if (!renorm) {
-            // plain softmax probability: divide by the sum over all E experts
-            double z = 0.0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (lane + 64 * i < E) z += exp((double)logit[i] - m);
-            wsum = wave_sum_f64(z);
-        }
+        w = exp((double)from_ordered_bits(my_key) - (double)from_ordered_bits(first_key));
     }
-    const double sc = (double)a.scaling;
+    if (lane >= k) w = 0.0;
+    if (method == MOE_ROUTE_LLAMA4) {
+        wsum = 1.0;
+    } else if (method == MOE_ROUTE_DEFAULT && !(a.flags & MOE_ROUTE_FLAG_RENORMALIZE)) {
+        // plain softmax probability: divide by the sum over all E experts
+        double z = 0.0;
 #pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j) scale[j] = (float)(w[j] / wsum * sc);
+        for (int i = 0; i < 4; ++i)
+            if (lane + 64 * i < E) z += exp((double)logit[i] - (double)from_ordered_bits(first_key));
+        wsum = wave_sum_f64(z);
+    } else {
+#pragma unroll
+        for (int j = 0; j < MOE_MAX_TOPK; ++j) wsum += __shfl(w, j, 64);
+        if (dsv3) wsum += 1e-20;
+    }
+    my_scale = (float)(w / wsum * (double)a.scaling);
 }
 
 }  // namespace

@@ -30,15 +30,13 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a, int32_t* __rest
     const int lane = threadIdx.x & 63;
     const int t = blockIdx.x * kWaves + wave;
     if (t >= a.T) return;  // a wave's LDS is its own: nothing waits for it
-    int id[MOE_MAX_TOPK];
-    float scale[MOE_MAX_TOPK];
-    route_token<true>(a, t, lane, s[wave], id, scale);
-#pragma unroll
-    for (int j = 0; j < MOE_MAX_TOPK; ++j) {
-        if (j < a.k && lane == j) {
-            ids[(size_t)t * a.k + j] = id[j];
-            scales[(size_t)t * a.k + j] = scale[j];
-        }
+    float logit[4], scale;
+    int id;
+    load_logits(a, t, lane, logit);
+    route_token<true>(a, logit, lane, s[wave], id, scale);
+    if (lane < a.k) {
+        ids[(size_t)t * a.k + lane] = id;
+        scales[(size_t)t * a.k + lane] = scale;
     }
 }
 

@@ -51,10 +51,10 @@ def test_validation(L):
             if other != out:
                 assert f(**{**full, out: value}) == INVALID and "same buffer" in binding.last_error(), (out, other)
     assert f(ws=None) == WORKSPACE
-    need = 4 * 2 * 128 * 2
-    assert f(n=need - 1) == WORKSPACE
     size = L.moe_layer_few_workspace_size
-    assert size(4, 256, 128, 8, 2, 0, BF16) == need and size(4, 256, 128, 8, 2, 1, F32) == 4 * 3 * 128 * 4
+    need = size(4, 256, 128, 8, 2, 0, BF16)
+    assert f(n=need - 1) == WORKSPACE
+    assert need >= 4 * 2 * 128 * 2 and size(4, 256, 128, 8, 2, 1, F32) >= 4 * 3 * 128 * 4  # h and what goes with it
     assert size(0, 256, 128, 8, 2, 0, BF16) == 0 and size(33, 256, 128, 8, 2, 0, BF16) == 0
     assert size(4, 256, 100, 8, 2, 0, BF16) == 0 and size(4, 256, 128, 8, 2, 0, FP8) == 0
     assert f(T=0, x=None, ws=None) == OK

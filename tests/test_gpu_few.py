@@ -64,12 +64,13 @@ class Layer:
         a = dict(self.gpu(), **change)
         T = a["x"].shape[0]
         bufs = out((T, self.H), self.dt), out((T, self.k), torch.int32), out((T, self.k), FP)
-        n = T * (self.k + self.sh) * self.I * bufs[0].element_size()
+        n = moe.layer_few_workspace(T, self.H, self.I, self.E, self.k, self.sh, self.dt).numel()
         ws = out((n,), U8)
         got = moe.layer_few(**a, ws=ws, out=bufs)
         assert all(p is q for p, q in zip(got, bufs))
         out.check()
-        return got, ws.view(self.dt).view(-1, self.I)
+        h = ws[:T * (self.k + self.sh) * self.I * bufs[0].element_size()]
+        return got, h.view(self.dt).view(-1, self.I)
 
     def check(self):
         (y, ids, scales), h = self.run()
