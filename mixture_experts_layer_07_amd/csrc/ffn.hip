@@ -461,8 +461,11 @@ __global__ __launch_bounds__(C::NT) void grouped_gemm_kernel(FfnArgs a)
 // LDS read a row for both steps, selected by the instruction (op_sel).  The
 // staged order of a row's 16-byte chunks is permuted to match (virtual chunk
 // 4b + g holds block 2g + b), and then swizzled like the others.  The scales of
-// the stage's BM + BN rows, 8 bytes each, are staged by 4-byte transfers spread
-// over the waves.  K is a multiple of 128: in a last stage of 128 values lane
+// two stages, 16 bytes of each of the BM + BN rows, go together, one transfer a lane
+// (every row is a line of its own to the caches, and their requests, not bytes, are
+// what the scales cost: with 8 bytes a stage in two 4-byte transfers FC1 of a decode
+// batch took 804 us, without any scales 656, now @DEC@), into one of two buffers
+// beside the ring.  K is a multiple of 128: in a last stage of 128 values lane
 // groups 2 and 3 read what groups 0 and 1 read, and their activations count as
 // zeros.  FC1's epilogue quantises h per row and 32 channels inside a wave; the
 // staged weight rows are ordered so that a lane holds eight neighbouring ones.
@@ -482,21 +485,23 @@ struct DmaCfg {
     static constexpr int B_OPS = BN * BROWB / 1024;        // ... and weights
     static constexpr int A_BYTES = BM * 128;
     static constexpr int B_BYTES = BN * BROWB;
-    static constexpr int S_OPS = A4 ? (BM + BN) / 32 : 0;  // 256-byte scale transfers per stage
-    static constexpr int IPW_S = A4 ? (S_OPS + NW - 1) / NW : A8 ? 1 : 0;  // ... per wave
-    static constexpr int SA_BYTES = A8 ? NW * 256 : S_OPS * 256;  // A8: per-wave slots
+    static constexpr int SA_BYTES = A8 ? NW * 256 : 0;     // A8: per-wave activation-scale slots
+    // A4: 1 KB scale transfers (64 rows) for two stages, and how many a wave does
+    static constexpr int S_OPS = A4 ? (BM + BN + 63) / 64 : 0;
+    static constexpr int IPW_S = (S_OPS + NW - 1) / NW;
     static constexpr int STAGE = A_BYTES + B_BYTES + SA_BYTES;  // bytes per stage
     static constexpr int NINS = A_OPS + B_OPS;
     static constexpr int IPW_AB = NINS / NW;               // 1 KB ops per wave per stage
-    static constexpr int IPW = IPW_AB + IPW_S;             // ... plus the scale transfers
+    static constexpr int IPW = IPW_AB + (A8 ? 1 : 0);      // ... plus the scale transfer
+    static constexpr int RING = S * STAGE + 2 * S_OPS * 1024;  // A4: the scales' buffers beside the ring
     static constexpr int WTM = BM / WM, WTN = BN / WN;
     static constexpr int MI = WTM / 16, NI = WTN / 16;
     static constexpr int AMAX_BYTES = A8 ? BM * WN * 4 : 4;  // FC1 epilogue: row maxima per wave column
     static_assert(BM % 8 == 0 && NINS % NW == 0 && IPW_AB >= 1, "DMA ops split evenly over waves");
     static_assert(WTM % 16 == 0 && WTN % 32 == 0, "tile");
     static_assert(!A8 || (WTM <= 64 && BN == 256), "A8: one scale transfer per wave; 128 h columns per tile");
-    static_assert(!A4 || (!W8_ && !A8 && BM % 32 == 0 && WTN % 64 == 0), "A4: whole scale transfers; 32 h columns per wave");
-    static_assert(S >= 2 && S <= 8 && S * STAGE + AMAX_BYTES <= 156 * 1024,
+    static_assert(!A4 || (!W8_ && !A8 && BM % 32 == 0 && WTN % 64 == 0 && S <= 4), "A4: 32 h columns per wave; the waits' count");
+    static_assert(S >= 2 && S <= 8 && RING + AMAX_BYTES <= 157 * 1024,
                   "ring (LDS also holds the tile tables)");
 };
 
@@ -504,7 +509,7 @@ struct DmaCfg {
 template <int MODE, class C>
 __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
 {
-    __shared__ __attribute__((aligned(1024))) char lds[C::S * C::STAGE];
+    __shared__ __attribute__((aligned(1024))) char lds[C::RING];
     __shared__ int s_off[kMaxGroups + 1];
     __shared__ int s_tile0[kMaxGroups + 1];
     __shared__ float s_amax[C::AMAX_BYTES / 4];  // A8 FC1 epilogue: [BM][WN] row maxima
@@ -564,11 +569,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
     // holds logical chunk physical ^ swizzle(row).  With fp8 activations op
     // q = IPW_AB of every wave stages the activation scales of the wave's own
     // rows: lane l fetches the scale of row wm*WTM + l % WTM.
-    // A4's scale op o (of S_OPS, spread over the waves; the last ones may be done
-    // twice) stages the 8 bytes of activation rows 32o .. 32o+31, then of weight
-    // rows: lane l half l % 2 of row l / 2.
-    auto op_is_s = [&](int q) { return (C::A8 || C::A4) && q >= C::IPW_AB; };
-    auto s_op = [&](int q) { return min((q - C::IPW_AB) * C::NW + wave, C::S_OPS - 1); };
+    auto op_is_s = [&](int q) { return C::A8 && q == C::IPW_AB; };
     auto op_is_a = [&](int q) { return q < C::IPW_AB && q * C::NW + wave < C::A_OPS; };
     auto op_row = [&](int q) {  // A row, or B row, of this lane in op q < IPW_AB
         const int o = q * C::NW + wave;
@@ -583,9 +584,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
         if (op_is_a(q) || !C::WNARROW) return (lane & 7) ^ (row & 7);
         return (lane & 3) ^ ((row >> 2) & 3);
     };
-    auto s_row = [&](int q) {  // scale op: this lane's tile row (A4: past BM, weight rows)
-        return C::A4 ? s_op(q) * 32 + (lane >> 1) : wm * C::WTM + lane % C::WTM;
-    };
+    const int s_row = wm * C::WTM + lane % C::WTM;  // scale op: this lane's tile row
     // the weight row that row j of the staged B tile holds
     auto weight_row = [&](const TileInfo& ti, int j) {
         if (MODE == FC1) {
@@ -603,7 +602,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
     // next tile's loads can be issued early and consumed a whole tile later.
     auto a_raw = [&](const TileInfo& ti, int q) -> int {
         if (MODE == FC2 || !(op_is_a(q) || op_is_s(q))) return 0;
-        const int rr = ti.m0 + (op_is_s(q) ? s_row(q) : op_row(q));
+        const int rr = ti.m0 + (op_is_s(q) ? s_row : op_row(q));
         const int i = (ti.g < a.E && rr < ti.nrows) ? ti.row0 + rr : 0;
         // global-space load: a flat load would also count in lgkmcnt and make
         // the LDS-only barriers wait for it
@@ -613,9 +612,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
     // (a_src), this tile's group of weights (wbase) or the activation scales.
     auto source = [&](const TileInfo& ti, int q, int raw) -> uint32_t {
         if (op_is_s(q)) {
-            if (C::A4 && s_op(q) * 32 >= C::BM)
-                return (uint32_t)weight_row(ti, s_row(q) - C::BM) * (uint32_t)(a.K / 32) + (lane & 1) * 4;
-            const int rr = ti.m0 + s_row(q);
+            const int rr = ti.m0 + s_row;
             long r;
             if (MODE == FC1) {
                 const int tok = (rr >= ti.nrows) ? 0 : (ti.g < a.E ? raw / a.k : rr);
@@ -623,7 +620,6 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
             } else {
                 r = ti.row0 + (rr < ti.nrows ? rr : 0);
             }
-            if constexpr (C::A4) return (uint32_t)(r * (a.K / 32)) + (lane & 1) * 4;
             return (uint32_t)(r * (a.K / 128) * 4);
         }
         const int row = op_row(q);
@@ -653,7 +649,65 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
     const char* wsbase = nullptr;  // ... and their scales
     uint32_t src[C::IPW];
     // A4: what a lane of groups 2 and 3 goes back in a last stage of 128 values
-    const uint32_t back = C::A4 && op_chunk(0, lane >> 3) >= 4 ? 64 : 0, sback = (lane & 1) * 4;
+    const uint32_t back = C::A4 && op_chunk(0, lane >> 3) >= 4 ? 64 : 0;
+
+    // A4's scales.  Op o (of S_OPS, spread over the waves, the last ones done twice
+    // where they do not divide) brings 16 bytes of rows 64o .. 64o+63, activations
+    // then weights, a lane each.  Rows that are no multiple of 16 bytes (K of 512)
+    // come in four 4-byte transfers instead, dword i of every row in plane i of the
+    // op's kilobyte; past the row's end its last dword again.
+    constexpr int kS = C::IPW_S > 0 ? C::IPW_S : 1;
+    const bool wide = a.K % 512 == 0;
+    const int nchunks = (nk + 1) / 2;
+    uint32_t ssrc[kS];
+    auto s_op = [&](int q) { return min(q * C::NW + wave, C::S_OPS - 1); };
+    auto s_raw = [&](const TileInfo& ti, int q) -> int {  // as a_raw
+        const int rr = ti.m0 + s_op(q) * 64 + lane;
+        const int i = (MODE == FC1 && ti.g < a.E && rr < ti.nrows) ? ti.row0 + rr : 0;
+        return MODE == FC2 ? 0 : *(const __attribute__((address_space(1))) int*)(a.permuted_pair + i);
+    };
+    auto s_source = [&](const TileInfo& ti, int q, int raw) -> uint32_t {
+        const int row = s_op(q) * 64 + lane;
+        uint32_t r;
+        if (row < C::BM) {
+            const int rr = ti.m0 + row;
+            if (MODE == FC1) {
+                const int tok = (rr >= ti.nrows) ? 0 : (ti.g < a.E ? raw / a.k : rr);
+                r = tok < 0 ? 0 : (tok >= a.T ? a.T - 1 : tok);
+            } else {
+                r = ti.row0 + (rr < ti.nrows ? rr : 0);
+            }
+            return r * (uint32_t)(a.K / 32);
+        }
+        return (uint32_t)weight_row(ti, min(row - C::BM, C::BN - 1)) * (uint32_t)(a.K / 32);
+    };
+    // An op's rows are activations or weights, but for BM = 32, where the lanes of op 0
+    // take each its own base.
+    auto issue_scales = [&](int j) {
+        const unsigned at = lds_base + C::S * C::STAGE + (j & 1) * (C::S_OPS * 1024);
+#pragma unroll
+        for (int q = 0; q < C::IPW_S; ++q) {
+            const int o = s_op(q);
+            auto one = [&](const char* base) {
+                if (wide) {
+                    dma16(__builtin_amdgcn_readfirstlane(at + o * 1024), base, ssrc[q] + j * 16);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dma4(__builtin_amdgcn_readfirstlane(at + o * 1024 + i * 256), base,
+                             ssrc[q] + min(j * 16 + i * 4, a.K / 32 - 4));
+                }
+            };
+            if constexpr (C::BM % 64 == 0) {
+                one(o * 64 < C::BM ? sbase : wsbase);
+            } else {
+                if (o > 0) one(wsbase);
+                else if (lane < C::BM) one(sbase);
+                else one(wsbase);
+            }
+        }
+    };
+    const int s_ops = C::IPW_S * (wide ? 1 : 4);
     auto issue = [&](int st, int kt) {
         const bool half = half_last && kt == nk - 1;
 #pragma unroll
@@ -661,19 +715,16 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
             dma16(__builtin_amdgcn_readfirstlane(lds_base + st * C::STAGE + (q * C::NW + wave) * 1024),
                   op_is_a(q) ? abase : wbase,
                   src[q] + (uint32_t)kt * (op_is_a(q) ? 128u : (uint32_t)C::BROWB) - (half ? back : 0u));
-        if constexpr (C::A4) {
-#pragma unroll
-            for (int q = C::IPW_AB; q < C::IPW; ++q)
-                dma4(__builtin_amdgcn_readfirstlane(lds_base + st * C::STAGE + C::A_BYTES + C::B_BYTES + s_op(q) * 256),
-                     s_op(q) * 32 < C::BM ? sbase : wsbase, src[q] + (uint32_t)kt * 8u - (half ? sback : 0u));
-        }
         if constexpr (C::A8)
             dma4(__builtin_amdgcn_readfirstlane(lds_base + st * C::STAGE + C::A_BYTES + C::B_BYTES + wave * 256),
                  sbase, src[C::IPW_AB] + (uint32_t)kt * 4u);
     };
     // this wave's transfers of a slice have landed while `later` newer slices'
     // transfers (IPW each) may still be in flight
-    auto wait_stage = [&](int later) { wait_vmcnt_le<(C::S - 2) * C::IPW>(later * C::IPW); };
+    // (A4: and the scales of the slice; `later_scales` transfers of later ones may be)
+    auto wait_stage = [&](int later, int later_scales = 0) {
+        wait_vmcnt_le<(C::S - 2) * C::IPW + 4 * C::IPW_S>(later * C::IPW + later_scales);
+    };
 
     TileInfo cur = decode_tile<C>(a, tile, s_off, s_tile0, G, ntiles_n);
     {
@@ -683,7 +734,12 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
 #pragma unroll
         for (int q = 0; q < C::IPW; ++q) src[q] = source(cur, q, idx[q]);
         wbase = group_weights(cur);
-        if constexpr (C::A4) wsbase = group_scales(cur);
+        if constexpr (C::A4) {
+            wsbase = group_scales(cur);
+#pragma unroll
+            for (int q = 0; q < C::IPW_S; ++q) ssrc[q] = s_source(cur, q, s_raw(cur, q));
+            issue_scales(0);
+        }
     }
     int ring = 0;  // ring slot of the current tile's slice 0
 #pragma unroll
@@ -694,11 +750,13 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
         const int next_tile = tile + nb;
         const bool has_next = next_tile < total;
         TileInfo nxt = cur;
-        int nidx[C::IPW];
+        int nidx[C::IPW], nsidx[kS];
         if (has_next) {
             nxt = decode_tile<C>(a, next_tile, s_off, s_tile0, G, ntiles_n);
 #pragma unroll
             for (int q = 0; q < C::IPW; ++q) nidx[q] = a_raw(nxt, q);
+#pragma unroll
+            for (int q = 0; q < C::IPW_S; ++q) nsidx[q] = s_raw(nxt, q);
         }
 
         f32x4_t acc[C::MI][C::NI];
@@ -715,8 +773,18 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
         }
 
         for (int kt = 0; kt < nk; ++kt) {
-            wait_stage(min(C::S - 2, nk - 1 - kt));
+            if constexpr (C::A4) {
+                // in an even step the next pair's scales go before the next slice: in
+                // an odd one they are younger than its slice where the ring holds three
+                const bool scales_later = C::S > 2 && (kt & 1) && (kt + 1) / 2 < nchunks;
+                wait_stage(min(C::S - 2, nk - 1 - kt), scales_later ? s_ops : 0);
+            } else {
+                wait_stage(min(C::S - 2, nk - 1 - kt));
+            }
             lds_barrier();  // slice kt is in LDS for every wave; slot of slice kt-1 is free
+            if constexpr (C::A4) {
+                if (!(kt & 1) && kt / 2 + 1 < nchunks) issue_scales(kt / 2 + 1);
+            }
             if (kt + C::S - 1 < nk) issue((ring + kt + C::S - 1) % C::S, kt + C::S - 1);
             const char* la = lds + ((ring + kt) % C::S) * C::STAGE;
             const char* lb = la + C::A_BYTES;
@@ -771,16 +839,19 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                 }
             } else if constexpr (C::A4) {
                 const int g4 = lane >> 4;
-                const char* ls = lb + C::B_BYTES;
+                const char* ls = lds + C::S * C::STAGE + ((kt >> 1) & 1) * (C::S_OPS * 1024);
+                // bytes 8 (kt % 2) + 2g of a row's sixteen
+                const int pair = (kt & 1) * 8 + g4 * 2;
+                const int at = wide ? pair : (pair >> 2) * 256 + (pair & 3), rs = wide ? 16 : 4;
+                auto scale_at = [&](int row) { return ls + (row >> 6) * 1024 + ((row & 63) + (lane & 15)) * rs + at; };
                 const bool none = half_last && kt == nk - 1 && g4 >= 2;  // past the row's end
                 int sa[C::MI], sw[C::NI];
 #pragma unroll
                 for (int mi = 0; mi < C::MI; ++mi)
-                    sa[mi] = *reinterpret_cast<const uint16_t*>(ls + (wm * C::WTM + mi * 16 + (lane & 15)) * 8 + g4 * 2);
+                    sa[mi] = *reinterpret_cast<const uint16_t*>(scale_at(wm * C::WTM + mi * 16));
 #pragma unroll
                 for (int ni = 0; ni < C::NI; ++ni)
-                    sw[ni] = *reinterpret_cast<const uint16_t*>(
-                        ls + (C::BM + wn * C::WTN + ni * 16 + (lane & 15)) * 8 + g4 * 2);
+                    sw[ni] = *reinterpret_cast<const uint16_t*>(scale_at(C::BM + wn * C::WTN + ni * 16));
                 auto kstep = [&](auto step) {
                     constexpr int b = decltype(step)::value;
                     u32x4_t fa[C::MI];
@@ -869,7 +940,12 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
 #pragma unroll
             for (int q = 0; q < C::IPW; ++q) src[q] = source(nxt, q, nidx[q]);
             wbase = group_weights(nxt);
-            if constexpr (C::A4) wsbase = group_scales(nxt);
+            if constexpr (C::A4) {
+                wsbase = group_scales(nxt);
+#pragma unroll
+                for (int q = 0; q < C::IPW_S; ++q) ssrc[q] = s_source(nxt, q, nsidx[q]);
+                issue_scales(0);
+            }
             ring = (ring + nk) % C::S;
 #pragma unroll
             for (int st = 0; st < C::S - 1; ++st)
