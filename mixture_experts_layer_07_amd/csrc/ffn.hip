@@ -466,8 +466,7 @@ __global__ __launch_bounds__(C::NT) void grouped_gemm_kernel(FfnArgs a)
 // what the scales cost: with 8 bytes a stage in two 4-byte transfers FC1 of a decode
 // batch took 804 us, without any scales 656, now @DEC@), into one of two buffers
 // beside the ring.  K is a multiple of 128: in a last stage of 128 values lane
-// groups 2 and 3 read what groups 0 and 1 read, and their activations count as
-// zeros.  FC1's epilogue quantises h per row and 32 channels inside a wave; the
+// groups 2 and 3 read what groups 0 and 1 read, and zeros for their activations.  FC1's epilogue quantises h per row and 32 channels inside a wave; the
 // staged weight rows are ordered so that a lane holds eight neighbouring ones.
 template <int BM_, int BN_, int WM_, int WN_, int GM_, int S_, bool W8_ = false, bool A8_ = false, bool A4_ = false>
 struct DmaCfg {
@@ -782,10 +781,13 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                 wait_stage(min(C::S - 2, nk - 1 - kt));
             }
             lds_barrier();  // slice kt is in LDS for every wave; slot of slice kt-1 is free
-            if constexpr (C::A4) {
-                if (!(kt & 1) && kt / 2 + 1 < nchunks) issue_scales(kt / 2 + 1);
-            }
-            if (kt + C::S - 1 < nk) issue((ring + kt + C::S - 1) % C::S, kt + C::S - 1);
+            auto issue_next = [&] {
+                if constexpr (C::A4) {
+                    if (!(kt & 1) && kt / 2 + 1 < nchunks) issue_scales(kt / 2 + 1);
+                }
+                if (kt + C::S - 1 < nk) issue((ring + kt + C::S - 1) % C::S, kt + C::S - 1);
+            };
+            if constexpr (!C::A4) issue_next();
             const char* la = lds + ((ring + kt) % C::S) * C::STAGE;
             const char* lb = la + C::A_BYTES;
             if constexpr (C::A8) {
@@ -844,34 +846,61 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                 const int pair = (kt & 1) * 8 + g4 * 2;
                 const int at = wide ? pair : (pair >> 2) * 256 + (pair & 3), rs = wide ? 16 : 4;
                 auto scale_at = [&](int row) { return ls + (row >> 6) * 1024 + ((row & 63) + (lane & 15)) * rs + at; };
-                const bool none = half_last && kt == nk - 1 && g4 >= 2;  // past the row's end
-                int sa[C::MI], sw[C::NI];
-#pragma unroll
-                for (int mi = 0; mi < C::MI; ++mi)
-                    sa[mi] = *reinterpret_cast<const uint16_t*>(scale_at(wm * C::WTM + mi * 16));
-#pragma unroll
-                for (int ni = 0; ni < C::NI; ++ni)
-                    sw[ni] = *reinterpret_cast<const uint16_t*>(scale_at(C::BM + wn * C::WTN + ni * 16));
-                auto kstep = [&](auto step) {
-                    constexpr int b = decltype(step)::value;
-                    u32x4_t fa[C::MI];
-#pragma unroll
-                    for (int mi = 0; mi < C::MI; ++mi) {
+                // Software pipeline: a weight fragment is read before the MI products in
+                // front of its own are issued, an activation fragment of the second
+                // K-step behind the last product with the first one's; the next slice's
+                // transfers go out behind the first reads.
+                if (half_last && kt == nk - 1) {
+                    // past the rows' end: zeros where groups 2 and 3 read activations
+                    for (int i = tid; i < C::BM * 4; i += C::NT) {
+                        const int row = i >> 2, v = (i & 2) * 2 + 2 + (i & 1);  // virtual chunks 2, 3, 6, 7
+                        *reinterpret_cast<u32x4_t*>(const_cast<char*>(la) + dma_off(row, v)) = u32x4_t{0u, 0u, 0u, 0u};
+                    }
+                    lds_barrier();
+                }
+                {
+                    int sa[C::MI], sw[C::NI];
+                    u32x4_t fa[C::MI], fb[2];
+                    auto read_a = [&](int b, int mi) {
                         fa[mi] = *reinterpret_cast<const u32x4_t*>(
                             la + dma_off(wm * C::WTM + mi * 16 + (lane & 15), 4 * b + g4));
-                        if (none) fa[mi] = u32x4_t{0u, 0u, 0u, 0u};
-                    }
-#pragma unroll
-                    for (int ni = 0; ni < C::NI; ++ni) {
-                        const u32x4_t fb = *reinterpret_cast<const u32x4_t*>(
+                    };
+                    auto read_b = [&](int b, int ni) {
+                        return *reinterpret_cast<const u32x4_t*>(
                             lb + dma_off(wn * C::WTN + ni * 16 + (lane & 15), 4 * b + g4));
+                    };
 #pragma unroll
-                        for (int mi = 0; mi < C::MI; ++mi)
-                            acc[mi][ni] = mfma_mxfp4<b>(fb, fa[mi], acc[mi][ni], sw[ni], sa[mi]);
+                    for (int mi = 0; mi < C::MI; ++mi) {
+                        sa[mi] = *reinterpret_cast<const uint16_t*>(scale_at(wm * C::WTM + mi * 16));
+                        read_a(0, mi);
                     }
-                };
-                kstep(std::integral_constant<int, 0>());
-                kstep(std::integral_constant<int, 1>());
+#pragma unroll
+                    for (int ni = 0; ni < C::NI; ++ni)
+                        sw[ni] = *reinterpret_cast<const uint16_t*>(scale_at(C::BM + wn * C::WTN + ni * 16));
+                    fb[0] = read_b(0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    issue_next();
+                    auto kstep = [&](auto step) {
+                        constexpr int b = decltype(step)::value;
+#pragma unroll
+                        for (int ni = 0; ni < C::NI; ++ni) {
+                            const int at = b * C::NI + ni;
+                            if (ni + 1 < C::NI) fb[(at + 1) & 1] = read_b(b, ni + 1);
+                            else if (b == 0) fb[(at + 1) & 1] = read_b(1, 0);
+#pragma unroll
+                            for (int mi = 0; mi < C::MI; ++mi) {
+                                acc[mi][ni] = mfma_mxfp4<b>(fb[at & 1], fa[mi], acc[mi][ni], sw[ni], sa[mi]);
+                                if (b == 0 && ni + 1 == C::NI) {
+                                    __builtin_amdgcn_sched_barrier(0);
+                                    read_a(1, mi);
+                                }
+                            }
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    };
+                    kstep(std::integral_constant<int, 0>());
+                    kstep(std::integral_constant<int, 1>());
+                }
             } else {
 #pragma unroll
             for (int ks = 0; ks < C::KSTEPS; ++ks) {
