@@ -144,6 +144,24 @@ __device__ __forceinline__ void store4_bf16(bf16_t* p, const float (&v)[4])
 }
 
 
+// silu(g) with e^-g as one v_exp_f32 of g times a rounded log2(e).  The product's
+// rounding moves silu by at most 0.44 of 2^-24 (g^2 s (1 - s) for s = sigmoid(g)),
+// less than the half-step that a gate of 1 has anyway, and expf costs the epilogue
+// of a 256x256 MXFP4 tile, which no product runs beside, @EXP@.
+__device__ __forceinline__ float silu_exp2(float g)
+{
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
+}
+
+// Maximum over the four lanes l, l ^ 16, l ^ 32, l ^ 48.
+__device__ __forceinline__ uint32_t max_over_groups(uint32_t m)
+{
+    const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+    m = max(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+    return max(b[0], b[1]);
+}
+
 // 16-byte load through the global address space.  The tile pointers live in
 // a by-value struct and loop-carried registers, where the compiler cannot infer
 // the address space and would emit flat loads, which also count against the
@@ -1053,11 +1071,10 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                     for (int i = 0; i < 8; ++i) {
                         const float gt = acc[mi][4 * b + (i >> 2) * 2][i & 3];
                         const float up = acc[mi][4 * b + (i >> 2) * 2 + 1][i & 3];
-                        hv[i] = gt * __builtin_amdgcn_rcpf(1.0f + expf(-gt)) * up;
+                        hv[i] = silu_exp2(gt) * up;
                         m = max(m, __float_as_uint(hv[i]) & 0x7fffffffu);
                     }
-                    m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-                    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+                    m = max_over_groups(m);
                     const uint32_t sc = mxfp4_scale(m);
                     if (rr < cur.nrows) {
                         const int blk = cur.nt * (C::BN / 64) + wn * (C::WTN / 64) + b;  // of the row's I / 32
