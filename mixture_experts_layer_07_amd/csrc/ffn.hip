@@ -146,8 +146,9 @@ __device__ __forceinline__ void store4_bf16(bf16_t* p, const float (&v)[4])
 
 // silu(g) with e^-g as one v_exp_f32 of g times a rounded log2(e).  The product's
 // rounding moves silu by at most 0.44 of 2^-24 (g^2 s (1 - s) for s = sigmoid(g)),
-// less than the half-step that a gate of 1 has anyway, and expf costs the epilogue
-// of a 256x256 MXFP4 tile, which no product runs beside, @EXP@.
+// less than the half-step that a gate of 1 has anyway, and expf costs more
+// where no product runs beside: the epilogue of 256x256 MXFP4 tiles (FC1 of 4096
+// tokens of the Mixtral-shaped layer 610 -> 553 us).
 __device__ __forceinline__ float silu_exp2(float g)
 {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
@@ -482,7 +483,7 @@ __global__ __launch_bounds__(C::NT) void grouped_gemm_kernel(FfnArgs a)
 // two stages, 16 bytes of each of the BM + BN rows, go together, one transfer a lane
 // (every row is a line of its own to the caches, and their requests, not bytes, are
 // what the scales cost: with 8 bytes a stage in two 4-byte transfers FC1 of a decode
-// batch took 804 us, without any scales 656, now @DEC@), into one of two buffers
+// batch took 804 us, without any scales 656, now 730), into one of two buffers
 // beside the ring.  K is a multiple of 128: in a last stage of 128 values lane
 // groups 2 and 3 read what groups 0 and 1 read, and zeros for their activations.  FC1's epilogue quantises h per row and 32 channels inside a wave; the
 // staged weight rows are ordered so that a lane holds eight neighbouring ones.
@@ -799,13 +800,10 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                 wait_stage(min(C::S - 2, nk - 1 - kt));
             }
             lds_barrier();  // slice kt is in LDS for every wave; slot of slice kt-1 is free
-            auto issue_next = [&] {
-                if constexpr (C::A4) {
-                    if (!(kt & 1) && kt / 2 + 1 < nchunks) issue_scales(kt / 2 + 1);
-                }
-                if (kt + C::S - 1 < nk) issue((ring + kt + C::S - 1) % C::S, kt + C::S - 1);
-            };
-            if constexpr (!C::A4) issue_next();
+            if constexpr (C::A4) {
+                if (!(kt & 1) && kt / 2 + 1 < nchunks) issue_scales(kt / 2 + 1);
+            }
+            if (kt + C::S - 1 < nk) issue((ring + kt + C::S - 1) % C::S, kt + C::S - 1);
             const char* la = lds + ((ring + kt) % C::S) * C::STAGE;
             const char* lb = la + C::A_BYTES;
             if constexpr (C::A8) {
@@ -866,8 +864,9 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                 auto scale_at = [&](int row) { return ls + (row >> 6) * 1024 + ((row & 63) + (lane & 15)) * rs + at; };
                 // Software pipeline: a weight fragment is read before the MI products in
                 // front of its own are issued, an activation fragment of the second
-                // K-step behind the last product with the first one's; the next slice's
-                // transfers go out behind the first reads.
+                // K-step behind the last product with the first one's.  (Left to the
+                // compiler every fragment was waited for where it was read: 1031 against
+                // 957 us for 4096 tokens of the Mixtral-shaped layer.)
                 if (half_last && kt == nk - 1) {
                     // past the rows' end: zeros where groups 2 and 3 read activations
                     for (int i = tid; i < C::BM * 4; i += C::NT) {
@@ -897,7 +896,6 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                         sw[ni] = *reinterpret_cast<const uint16_t*>(scale_at(C::BM + wn * C::WTN + ni * 16));
                     fb[0] = read_b(0, 0);
                     __builtin_amdgcn_sched_barrier(0);
-                    issue_next();
                     auto kstep = [&](auto step) {
                         constexpr int b = decltype(step)::value;
 #pragma unroll
