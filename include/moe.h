@@ -610,8 +610,10 @@ moe_status moe_expert_ffn_mxfp4(const uint8_t* xq, const uint8_t* x_scale, int T
  *  ids, scales   device int32, fp32 [T, k] out.
  *  y         device [T, H] out in `act`.
  *  ws        device workspace of moe_layer_few_workspace_size(...) bytes; on
- *            return it holds h [T*k + n_shared*T, I], rows in moe_permute's order.
- * H and I are multiples of 128, at most 2^20.  x, the weights, their scales, y
+ *            return it holds h [T*k + n_shared*T, I], rows in moe_permute's order,
+ *            and the plan that the second kernel reads.
+ * H and I are multiples of 128, at most 2^20; h and one expert's w13 are below
+ * 4 GiB (MOE_ERR_UNSUPPORTED).  x, the weights, their scales, y
  * and ws are 16-byte aligned; no output is an input or another output.  The same
  * inputs give the same bits.  ids, scales and h of a token do not depend on the
  * other tokens; y's order of summation does, unless I is a multiple of 1024.

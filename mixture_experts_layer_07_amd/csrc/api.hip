@@ -733,6 +733,9 @@ static moe_status check_few(int T, int H, int I, int E, int k, int n_shared, int
     if (wdt < MOE_F32 || wdt > MOE_MXFP4) return set_error(MOE_ERR_INVALID_ARG, "unknown weight dtype %d", wdt);
     if ((act == MOE_F32) != (wdt == MOE_F32))
         return set_error(MOE_ERR_UNSUPPORTED, "fp32 activations go with fp32 weights, bf16 ones with the others");
+    // the kernels' offsets into h, and into one expert's matrix, have 32 bits
+    if ((uint64_t)T * (k + n_shared) * I * (act == MOE_F32 ? 4 : 2) >> 32)
+        return set_error(MOE_ERR_UNSUPPORTED, "h of %d rows of %d exceeds 4 GiB", T * (k + n_shared), I);
     return MOE_OK;
 }
 
@@ -750,7 +753,11 @@ moe_status moe_layer_few(const void* x, int act, const float* logits, int T, int
 {
     moe_status st = check_few(T, H, I, E, k, n_shared, act, wdt);
     if (st == MOE_OK) st = check_route(T, E, method, k, n_group, topk_group, scaling, flags);
-    if (st != MOE_OK || T == 0) return st;
+    if (st != MOE_OK) return st;
+    const uint64_t halves = wdt == MOE_F32 ? 8 : wdt == MOE_BF16 ? 4 : wdt == MOE_FP8_E4M3 ? 2 : 1;  // bytes of two weights
+    if ((uint64_t)I * H * halves >> 32)
+        return set_error(MOE_ERR_UNSUPPORTED, "one expert's w13 (2 x %d x %d) exceeds 4 GiB", I, H);
+    if (T == 0) return MOE_OK;
     if (!x || !logits || !w13 || !w2 || !ids || !scales || !y)
         return set_error(MOE_ERR_INVALID_ARG, "x, logits, w13, w2, ids, scales and y must be non-null");
     const bool scaled = wdt == MOE_FP8_E4M3 || wdt == MOE_MXFP4;

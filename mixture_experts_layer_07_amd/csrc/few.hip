@@ -514,7 +514,7 @@ __device__ __forceinline__ void fc2_tiles(const FewArgs& a, const Plan& plan, Co
             const Chunk c = get_chunk(plan, chunk);
             ahead.chunk = chunk;
             ahead.e = c.e;
-            ahead.vat = (uint32_t)(c.row0 * a.I) * (uint32_t)sizeof(act);
+            ahead.vat = (uint32_t)c.row0 * (uint32_t)a.I * (uint32_t)sizeof(act);  // h is under 4 GiB
 #pragma unroll
             for (int i = 0; i < P::VL; ++i)
                 ahead.voff[i] = (uint32_t)(min(P::token(lane, i), c.n - 1) * a.I) * (uint32_t)sizeof(act) + P::chunk16(lane);

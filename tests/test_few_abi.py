@@ -33,6 +33,15 @@ def test_validation(L):
     assert f(E_=300) == UNSUPPORTED and f(E_=64, k=9) == UNSUPPORTED
     assert f(H=0) == INVALID and f(I_=-128) == INVALID and f(H=192) == UNSUPPORTED and f(I_=64) == UNSUPPORTED
     assert f(H=(1 << 20) + 128) == UNSUPPORTED
+    # one expert's w13 and h have to be under 4 GiB (T = 0: nothing else is looked at)
+    big, n = 1 << 20, 1 << 40
+    for wdt, rows in ((F32, 512), (BF16, 1024), (FP8, 2048), (MX, 4096)):
+        how = dict(act=F32 if wdt == F32 else BF16, wdt=wdt, T=0, H=big)
+        assert f(**how, I_=rows) == UNSUPPORTED and "w13" in binding.last_error(), wdt
+        assert f(**how, I_=rows - 128) == OK, wdt
+    assert f(T=32, k=8, E_=64, sh=56, H=128, I_=big, n=n) == UNSUPPORTED and "h of 2048 rows" in binding.last_error()
+    assert L.moe_layer_few_workspace_size(32, 128, big, 64, 8, 56, BF16) == 0
+    assert L.moe_layer_few_workspace_size(32, 128, big - 128, 64, 8, 56, BF16) > (1 << 32) - (1 << 20)
     assert f(act=FP8) == INVALID and f(act=MX) == INVALID and f(wdt=4) == INVALID and f(wdt=-1) == INVALID
     assert f(act=F32) == UNSUPPORTED and f(wdt=F32) == UNSUPPORTED and f(act=F32, wdt=MX) == UNSUPPORTED
     # the routing's own refusals

@@ -328,6 +328,23 @@ def test_large_weights():
     assert far < 2 * half_step(BF), far  # h and y rounded
 
 
+def test_offsets_past_2_31_in_one_expert():
+    """w13 just under 4 GiB, the largest that is taken."""
+    g = torch.Generator(device=DEV).manual_seed(0)
+    H, I = 1024, (1 << 20) - 128
+    w13 = torch.empty((1, 2 * I, H), dtype=BF, device=DEV).normal_(0, H ** -0.5, generator=g)
+    w2 = torch.empty((1, H, I), dtype=BF, device=DEV).normal_(0, I ** -0.5, generator=g)
+    x = torch.randn((2, H), generator=g, device=DEV).to(BF)
+    y, _, sc = moe.layer_few(x, torch.zeros((2, 1), device=DEV), w13, w2, 1, RENORM)
+    want = torch.zeros(2, H, dtype=F64, device=DEV)
+    for at in range(0, I, 1 << 17):
+        part = slice(at, min(at + (1 << 17), I))
+        h = torch.nn.functional.silu(x.double() @ w13[0, :I][part].double().t()) * (x.double() @ w13[0, I:][part].double().t())
+        want += h @ w2[0, :, part].double().t()
+    far = float((y.double() - want).norm() / want.norm())
+    assert far < 2 * half_step(BF), far  # h and y rounded
+
+
 def test_empty_and_refusals():
     a = Layer(4, 256, 128, 8, 2, "bf16")
     g = a.gpu()
