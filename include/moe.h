@@ -616,7 +616,8 @@ moe_status moe_expert_ffn_mxfp4(const uint8_t* xq, const uint8_t* x_scale, int T
  * 4 GiB (MOE_ERR_UNSUPPORTED).  x, the weights, their scales, y
  * and ws are 16-byte aligned; no output is an input or another output.  The same
  * inputs give the same bits.  ids, scales and h of a token do not depend on the
- * other tokens; y's order of summation does, unless I is a multiple of 1024.
+ * other tokens; y's order of summation does, unless I is a multiple of 1024 (512
+ * for fp32 weights, 2048 for MXFP4).
  * NaN logits of a token give unspecified values in that token's rows.
  */
 moe_status moe_layer_few(const void* x, int act, const float* logits, int T, int H, int I, int E, int method,

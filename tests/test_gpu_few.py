@@ -158,11 +158,14 @@ def test_equal_logits_and_infinities():
     Layer(20, 128, 128, 40, 4, "bf16", logits=l).check()
 
 
-@pytest.mark.parametrize("wdt", WDT)
-def test_a_token_alone(wdt):
-    """ids, weights and h of a token are the same alone and among others, and so is y where I is a
-    multiple of 1024."""
-    a = Layer(19, 256, 1024, 16, 4, wdt, 1)
+# the I whose rows give every wave as many pieces: y's order of summation is the token's own
+EVEN_I = [("f32", 512), ("bf16", 1024), ("fp8", 1024), ("mxfp4", 2048)]
+
+
+@pytest.mark.parametrize("wdt,I", EVEN_I)
+def test_a_token_alone(wdt, I):
+    """ids, weights and h of a token are the same alone and among others, and so is y at these I."""
+    a = Layer(19, 256, I, 16, 4, wdt, 1)
     (y, ids, scales), h = a.run()
     g = a.gpu()
     _, _, up = oracle.permute(ids.cpu().numpy(), a.E, 1)
@@ -177,9 +180,9 @@ def test_a_token_alone(wdt):
         same(y1[0], y[t], "y")
 
 
-@pytest.mark.parametrize("wdt", WDT)
-def test_nan_stays_with_its_token(wdt):
-    a = Layer(12, 256, 128, 8, 2, wdt, 1)
+@pytest.mark.parametrize("wdt,I", EVEN_I)
+def test_nan_stays_with_its_token(wdt, I):
+    a = Layer(12, 256, I, 8, 2, wdt, 1)
     (clean, ids, _), _ = a.run()
     bad = a.x.clone()
     bad[5, 17] = float("nan")
@@ -195,6 +198,22 @@ def test_nan_stays_with_its_token(wdt):
     rest = [t for t in range(12) if t != 2]
     same(y[rest], clean[rest], "other tokens")
     assert bool(((i3 >= 0) & (i3 < 8)).all())
+
+
+def test_a_token_with_every_expert_masked():
+    """moe_route's ids and weights for it, and the other tokens' results as they were."""
+    for method in range(7):
+        a = Layer(9, 128, 1024, 32, 4, "bf16", method=method)
+        (clean, _, _), _ = a.run()
+        l = a.logits.clone()
+        l[4] = float("-inf")
+        g = dict(a.gpu(), logits=l.to(DEV))
+        (y, ids, scales), _ = a.run(logits=g["logits"])
+        want = moe.route(g["logits"], 4, method)
+        same(ids, want[0], "ids")
+        same(scales, want[1], "scales")
+        rest = [t for t in range(9) if t != 4]
+        same(y[rest], clean[rest], "other tokens")
 
 
 def test_weights_that_no_token_chooses_are_not_read():
