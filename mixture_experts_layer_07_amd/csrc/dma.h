@@ -75,6 +75,16 @@ __device__ __forceinline__ void dma16(unsigned lds_addr, const char* base, uint3
                  :: "s"(lds_addr), "v"(off), "s"(base) : "memory", "m0");
 }
 
+// The same if i < n (wave-uniform), without a branch that the compiler sees: it would
+// move products that stand in front of one behind it.
+__device__ __forceinline__ void dma16_below(int i, int n, unsigned lds_addr, const char* base, uint32_t off)
+{
+    asm volatile("s_cmp_ge_i32 %3, %4\n\ts_cbranch_scc1 .Lno_dma%=\n\ts_mov_b32 m0, %0\n\t"
+                 "global_load_lds_dwordx4 %1, %2\n.Lno_dma%=:"
+                 :: "s"(lds_addr), "v"(off), "s"(base), "s"(__builtin_amdgcn_readfirstlane(i)),
+                    "s"(__builtin_amdgcn_readfirstlane(n)) : "memory", "m0", "scc");
+}
+
 // Same with 4 bytes per lane: lane l lands at byte 4*l of the 256 bytes at
 // `lds_addr`.
 __device__ __forceinline__ void dma4(unsigned lds_addr, const char* base, uint32_t off)
@@ -92,6 +102,7 @@ __device__ __forceinline__ const char* uniform_ptr(const char* p)
     return reinterpret_cast<const char*>(((uint64_t)hi << 32) | lo);
 }
 
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 // 16x16x128 MFMA on e4m3 codes (format 0 for both operands); its per-lane
@@ -102,14 +113,16 @@ __device__ __forceinline__ f32x4_t mfma_fp8(const i32x8_t& a, const i32x8_t& b)
                                                             127, 0, 127);
 }
 
-// 16x16x128 MFMA on e2m1 codes (format 4 for both operands), 32 a lane, with each
-// lane's E8M0 scale in byte B of its scale operand.
+// 32x32x64 MFMA on e2m1 codes (format 4 for both operands), 32 a lane, with each
+// lane's E8M0 scale in byte B of its scale operand.  (The 16x16x128 form cannot be
+// issued as fast as it multiplies: 29 cycles for 16 of work with one wave a SIMD,
+// 5.5 PFLOP/s over the chip and 6.9 with more waves, where this reaches 7.9 and 8.2.)
 template <int B>
-__device__ __forceinline__ f32x4_t mfma_mxfp4(const u32x4_t& a, const u32x4_t& b, const f32x4_t& c, int sa, int sb)
+__device__ __forceinline__ f32x16_t mfma_mxfp4(const u32x4_t& a, const u32x4_t& b, const f32x16_t& c, int sa, int sb)
 {
     const i32x8_t wa = {(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
     const i32x8_t wb = {(int)b.x, (int)b.y, (int)b.z, (int)b.w, 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wa, wb, c, 4, 4, B, sa, B, sb);
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wa, wb, c, 4, 4, B, sa, B, sb);
 }
 
 // Lane group g's 32 fp8 codes of one row of a staged 128-byte K block: logical

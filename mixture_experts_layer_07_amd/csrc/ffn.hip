@@ -154,15 +154,6 @@ __device__ __forceinline__ float silu_exp2(float g)
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
 }
 
-// Maximum over the four lanes l, l ^ 16, l ^ 32, l ^ 48.
-__device__ __forceinline__ uint32_t max_over_groups(uint32_t m)
-{
-    const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
-    m = max(a[0], a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
-    return max(b[0], b[1]);
-}
-
 // 16-byte load through the global address space.  The tile pointers live in
 // a by-value struct and loop-carried registers, where the compiler cannot infer
 // the address space and would emit flat loads, which also count against the
@@ -470,23 +461,27 @@ __global__ __launch_bounds__(C::NT) void grouped_gemm_kernel(FfnArgs a)
 // such block of every row).
 //
 // MXFP4 activations and weights (A4): a stage is 256 K values, 128-byte rows of
-// codes for both operands, two K-steps of v_mfma_f32_16x16x128_f8f6f4 that take
+// codes for both operands, four K-steps of v_mfma_f32_32x32x64_f8f6f4 that take
 // the scales themselves (one E8M0 byte a lane: a lane feeds 32 values of a row,
 // one scale block).  Its sums are good for fp32: products of e2m1 codes are small
-// integers, and chains of 64 steps over random scales came out 30 times nearer
-// to the exact sum than fp32 additions in order (3e-7 of the result's norm), so
-// blocks accumulate in the instruction.  Lane group g of K-step b takes 32-value
-// block 2g + b, so that a lane's two scales are neighbouring bytes: one 2-byte
-// LDS read a row for both steps, selected by the instruction (op_sel).  The
-// staged order of a row's 16-byte chunks is permuted to match (virtual chunk
-// 4b + g holds block 2g + b), and then swizzled like the others.  The scales of
-// two stages, 16 bytes of each of the BM + BN rows, go together, one transfer a lane
-// (every row is a line of its own to the caches, and their requests, not bytes, are
-// what the scales cost: with 8 bytes a stage in two 4-byte transfers FC1 of a decode
-// batch took 804 us, without any scales 656, now 730), into one of two buffers
-// beside the ring.  K is a multiple of 128: in a last stage of 128 values lane
-// groups 2 and 3 read what groups 0 and 1 read, and zeros for their activations.  FC1's epilogue quantises h per row and 32 channels inside a wave; the
-// staged weight rows are ordered so that a lane holds eight neighbouring ones.
+// integers, and chains of 64 steps over random scales came out nearer to the exact
+// sum than fp32 additions in order, so blocks accumulate in the instruction.
+// Lane half g of K-step b takes 32-value block 4g + b, so that a lane's four scales
+// are neighbouring bytes: one 4-byte LDS read a row for all steps, selected by the
+// instruction (op_sel).  The scales of two stages, 16 bytes of each of the BM + BN
+// rows, go together, one transfer a lane (every row is a line of its own to the
+// caches, and their requests, not bytes, are what the scales cost: with 8 bytes a
+// stage in two 4-byte transfers FC1 of a decode batch took 804 us, without any
+// scales 656, now 713), into one of two buffers beside the ring.  K is a multiple
+// of 128: in a last stage of 128 values half 1 reads what half 0 reads, and zeros
+// for its activations.  FC1's epilogue quantises h per row and 32 channels inside a
+// wave; the staged weight rows are ordered so that a lane holds sixteen neighbouring
+// ones.
+// What bounds the 256x256 tiles is power and LDS: 32x32x64 products of random codes
+// from registers run at 6.2 PFLOP/s on the whole chip, with the six fragments read
+// from LDS that eight of them take here at 5.3, and the K loop's share of FC1 (4096
+// tokens of the Mixtral-shaped layer, 3.4 PFLOP/s in all) comes to 4.7: the rest are
+// tiles' empty rows and the epilogue.
 template <int BM_, int BN_, int WM_, int WN_, int GM_, int S_, bool W8_ = false, bool A8_ = false, bool A4_ = false>
 struct DmaCfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GM = GM_, S = S_;
@@ -497,7 +492,7 @@ struct DmaCfg {
     static constexpr int NT = WM * WN * 64;
     static constexpr int NW = WM * WN;
     static constexpr int BK = A4 ? 256 : A8 ? 128 : 64;    // K per stage
-    static constexpr int KSTEPS = A8 ? 1 : A4 ? 2 : BK / 32;  // MFMA K-steps per stage
+    static constexpr int KSTEPS = A8 ? 1 : A4 ? 4 : BK / 32;  // MFMA K-steps per stage
     static constexpr int BROWB = WNARROW ? 64 : 128;       // weight bytes per staged row
     static constexpr int A_OPS = BM / 8;                   // 1 KB DMA ops per stage, activations
     static constexpr int B_OPS = BN * BROWB / 1024;        // ... and weights
@@ -513,7 +508,8 @@ struct DmaCfg {
     static constexpr int IPW = IPW_AB + (A8 ? 1 : 0);      // ... plus the scale transfer
     static constexpr int RING = S * STAGE + 2 * S_OPS * 1024;  // A4: the scales' buffers beside the ring
     static constexpr int WTM = BM / WM, WTN = BN / WN;
-    static constexpr int MI = WTM / 16, NI = WTN / 16;
+    static constexpr int MB = A4 ? 32 : 16;                // edge of an MFMA's result
+    static constexpr int MI = WTM / MB, NI = WTN / MB;
     static constexpr int AMAX_BYTES = A8 ? BM * WN * 4 : 4;  // FC1 epilogue: row maxima per wave column
     static_assert(BM % 8 == 0 && NINS % NW == 0 && IPW_AB >= 1, "DMA ops split evenly over waves");
     static_assert(WTM % 16 == 0 && WTN % 32 == 0, "tile");
@@ -595,24 +591,20 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
         return C::WNARROW ? (o - C::A_OPS) * 16 + (lane >> 2) : (o - C::A_OPS) * 8 + (lane >> 3);
     };
     auto op_chunk = [&](int q, int row) {  // logical 16-byte chunk this lane fetches
-        if constexpr (C::A4) {
-            const int v = (lane & 7) ^ (row & 7);  // virtual chunk 4b + g: block 2g + b
-            return 2 * (v & 3) + (v >> 2);
-        }
         if (op_is_a(q) || !C::WNARROW) return (lane & 7) ^ (row & 7);
         return (lane & 3) ^ ((row >> 2) & 3);
     };
     const int s_row = wm * C::WTM + lane % C::WTM;  // scale op: this lane's tile row
     // the weight row that row j of the staged B tile holds
     auto weight_row = [&](const TileInfo& ti, int j) {
+        // A4: a lane's results are rows 8q + 4g + i (q, i < 4) of a block, and these
+        // channels 16g + 4q + i
+        const int r = j % C::MB, ch = C::A4 ? ((r >> 2) & 1) * 16 + (r >> 3) * 4 + (r & 3) : r;
         if (MODE == FC1) {
-            const int blk = j >> 4, pair = blk >> 1, r = j & 15;
-            // A4: rows 4g + i of pairs 2b and 2b + 1 are channels 8g + i and 8g + 4 + i of block b
-            const int col = ti.nt * (C::BN / 2) +
-                            (C::A4 ? (pair >> 1) * 32 + (r >> 2) * 8 + (pair & 1) * 4 + (r & 3) : pair * 16 + r);
+            const int blk = j / C::MB, col = ti.nt * (C::BN / 2) + (blk >> 1) * C::MB + ch;
             return (blk & 1) ? a.I + col : col;
         }
-        return min(ti.nt * C::BN + j, a.N - 1);  // partial last N-tile
+        return min(ti.nt * C::BN + j - r + ch, a.N - 1);  // partial last N-tile
     };
 
     // For FC1 A rows the token comes from permuted_pair: a_raw() only loads the
@@ -666,7 +658,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
     const char* wbase;  // weights of the group whose slices `issue` sends
     const char* wsbase = nullptr;  // ... and their scales
     uint32_t src[C::IPW];
-    // A4: what a lane of groups 2 and 3 goes back in a last stage of 128 values
+    // A4: what a lane whose chunk is past the end goes back in a last stage of 128 values
     const uint32_t back = C::A4 && op_chunk(0, lane >> 3) >= 4 ? 64 : 0;
 
     // A4's scales.  Op o (of S_OPS, spread over the waves, the last ones done twice
@@ -726,13 +718,14 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
         }
     };
     const int s_ops = C::IPW_S * (wide ? 1 : 4);
+    auto issue_op = [&](int st, int kt, int q, auto send) __attribute__((always_inline)) {
+        send(__builtin_amdgcn_readfirstlane(lds_base + st * C::STAGE + (q * C::NW + wave) * 1024),
+             op_is_a(q) ? abase : wbase,
+             src[q] + (uint32_t)kt * (op_is_a(q) ? 128u : (uint32_t)C::BROWB) - (half_last && kt == nk - 1 ? back : 0u));
+    };
     auto issue = [&](int st, int kt) {
-        const bool half = half_last && kt == nk - 1;
 #pragma unroll
-        for (int q = 0; q < C::IPW_AB; ++q)
-            dma16(__builtin_amdgcn_readfirstlane(lds_base + st * C::STAGE + (q * C::NW + wave) * 1024),
-                  op_is_a(q) ? abase : wbase,
-                  src[q] + (uint32_t)kt * (op_is_a(q) ? 128u : (uint32_t)C::BROWB) - (half ? back : 0u));
+        for (int q = 0; q < C::IPW_AB; ++q) issue_op(st, kt, q, dma16);
         if constexpr (C::A8)
             dma4(__builtin_amdgcn_readfirstlane(lds_base + st * C::STAGE + C::A_BYTES + C::B_BYTES + wave * 256),
                  sbase, src[C::IPW_AB] + (uint32_t)kt * 4u);
@@ -741,7 +734,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
     // transfers (IPW each) may still be in flight
     // (A4: and the scales of the slice; `later_scales` transfers of later ones may be)
     auto wait_stage = [&](int later, int later_scales = 0) {
-        wait_vmcnt_le<(C::S - 2) * C::IPW + 4 * C::IPW_S>(later * C::IPW + later_scales);
+        wait_vmcnt_le<(C::S - (C::A4 ? 1 : 2)) * C::IPW + 4 * C::IPW_S>(later * C::IPW + later_scales);
     };
 
     TileInfo cur = decode_tile<C>(a, tile, s_off, s_tile0, G, ntiles_n);
@@ -757,6 +750,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
 #pragma unroll
             for (int q = 0; q < C::IPW_S; ++q) ssrc[q] = s_source(cur, q, s_raw(cur, q));
             issue_scales(0);
+            if (nchunks > 1) issue_scales(1);
         }
     }
     int ring = 0;  // ring slot of the current tile's slice 0
@@ -777,12 +771,13 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
             for (int q = 0; q < C::IPW_S; ++q) nsidx[q] = s_raw(nxt, q);
         }
 
-        f32x4_t acc[C::MI][C::NI];
+        using Acc = std::conditional_t<C::A4, f32x16_t, f32x4_t>;
+        Acc acc[C::MI][C::NI];
         f32x4_t part[C::WNARROW ? C::MI : 1][C::WNARROW ? C::NI : 1];  // fp8: this K block's sums
 #pragma unroll
         for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
-            for (int ni = 0; ni < C::NI; ++ni) acc[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            for (int ni = 0; ni < C::NI; ++ni) acc[mi][ni] = (Acc)(0.f);
         if constexpr (C::WNARROW) {
 #pragma unroll
             for (int mi = 0; mi < C::MI; ++mi)
@@ -790,19 +785,121 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                 for (int ni = 0; ni < C::NI; ++ni) part[mi][ni] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         }
 
-        for (int kt = 0; kt < nk; ++kt) {
-            if constexpr (C::A4) {
-                // in an even step the next pair's scales go before the next slice: in
-                // an odd one they are younger than its slice where the ring holds three
-                const bool scales_later = C::S > 2 && (kt & 1) && (kt + 1) / 2 < nchunks;
-                wait_stage(min(C::S - 2, nk - 1 - kt), scales_later ? s_ops : 0);
-            } else {
-                wait_stage(min(C::S - 2, nk - 1 - kt));
+        if constexpr (C::A4) {
+            // A slice is NP positions, a K-step and a weight fragment each, of MI products.
+            // Fragments are read ahead: weights three positions, activations a K-step;
+            // at position kTurn, when all of the slice has been read, the waves meet, the
+            // next slice's first fragments are read beside the last products, and its
+            // slot of the ring is filled again, a transfer or two beside each position of
+            // the next half slice (all at once they hold the waves up: 64 KB are 1024
+            // cycles of the CU's path to memory).  The loop starts at that place: where it
+            // lay inside, the compiler moved the products in front of its branches behind
+            // them.  Four waves of 128x128 read a third less from LDS, but have nothing to
+            // run beside an epilogue: FC1 759 against 583 us (4096 tokens of the
+            // Mixtral-shaped layer), FC2 337 against 327.
+            constexpr int NP = 4 * C::NI, kTurn = NP - 2;
+            const int g = lane >> 5, r32 = lane & 31, rs = wide ? 16 : 4;
+            const char *la, *lb, *ls;
+            u32x4_t fa[2][C::MI], fb[4];
+            int sa[2][C::MI], sw[2][C::NI];  // four scales, the K-steps'; [1]: the next slice's
+            auto enter = [&](int kt) __attribute__((always_inline)) {
+                la = lds + ((ring + kt) % C::S) * C::STAGE;
+                lb = la + C::A_BYTES;
+                const int at = (kt & 1) * 2 + g;  // dword of a row's four
+                ls = lds + C::S * C::STAGE + ((kt >> 1) & 1) * (C::S_OPS * 1024) + at * (wide ? 4 : 256);
+                if (half_last && kt == nk - 1) {  // zeros for the activations past the rows' end
+                    for (int i = tid; i < C::BM * 4; i += C::NT)
+                        *reinterpret_cast<u32x4_t*>(const_cast<char*>(la) + dma_off(i >> 2, 4 + (i & 3))) =
+                            u32x4_t{0u, 0u, 0u, 0u};
+                    lds_barrier();
+                }
+            };
+            auto read_a = [&](int b, int mi) __attribute__((always_inline)) {
+                fa[b & 1][mi] = *reinterpret_cast<const u32x4_t*>(la + dma_off(wm * C::WTM + mi * 32 + r32, 4 * g + b));
+            };
+            auto read_b = [&](int p) __attribute__((always_inline)) {
+                fb[p & 3] = *reinterpret_cast<const u32x4_t*>(
+                    lb + dma_off(wn * C::WTN + (p % C::NI) * 32 + r32, 4 * g + (p % NP) / C::NI));
+            };
+            auto read_scale = [&](int row) __attribute__((always_inline)) {
+                return *reinterpret_cast<const int*>(ls + (row >> 6) * 1024 + ((row & 63) + r32) * rs);
+            };
+            auto read_scales = [&](int to) __attribute__((always_inline)) {
+#pragma unroll
+                for (int mi = 0; mi < C::MI; ++mi) sa[to][mi] = read_scale(wm * C::WTM + mi * 32);
+#pragma unroll
+                for (int ni = 0; ni < C::NI; ++ni) sw[to][ni] = read_scale(C::BM + wn * C::WTN + ni * 32);
+            };
+            int fill = 0, fill_slot = 0;  // the slice to send, and where
+            auto position = [&](auto pp, auto more, auto send) __attribute__((always_inline)) {
+                constexpr int p = decltype(pp)::value, b = p / C::NI, ni = p % C::NI;
+                constexpr int t = decltype(send)::value ? (p + NP - kTurn) % NP : NP;
+#pragma unroll
+                for (int q = 0; q < C::IPW_AB; ++q)
+                    if (q * (NP / 2) / C::IPW_AB == t)
+                        issue_op(fill_slot, fill, q, [&](unsigned to, const char* base, uint32_t off) {
+                            dma16_below(fill, nk, to, base, off);
+                        });
+                if constexpr (p + 3 < NP) read_b(p + 3);
+                if constexpr (b < 3 && ni < C::NI / 2) {
+                    constexpr int n = 2 * C::MI / C::NI;
+#pragma unroll
+                    for (int i = 0; i < n; ++i) read_a(b + 1, ni * n + i);
+                }
+                if constexpr (p == kTurn && decltype(more)::value) {
+#pragma unroll
+                    for (int mi = 0; mi < C::MI; ++mi) read_a(0, mi);
+                    read_b(NP);
+                    read_b(NP + 1);
+                    read_scales(1);
+                }
+                if constexpr (p > kTurn && decltype(more)::value) read_b(NP + 2);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int mi = 0; mi < C::MI; ++mi)
+                    acc[mi][ni] = mfma_mxfp4<b>(fb[p & 3], fa[b & 1][mi], acc[mi][ni], sw[0][ni], sa[0][mi]);
+                __builtin_amdgcn_sched_barrier(0);
+            };
+            auto positions = [&]<int From, int... P>(std::integral_constant<int, From>, std::integer_sequence<int, P...>,
+                                                     auto more, auto send) __attribute__((always_inline)) {
+                (position(std::integral_constant<int, From + P>(), more, send), ...);
+            };
+            auto before_turn = [&](auto send) __attribute__((always_inline)) {
+                positions(std::integral_constant<int, 0>(), std::make_integer_sequence<int, kTurn>(), std::true_type(), send);
+            };
+            if (MODE == FC2) lds_barrier();  // the slot of the last epilogue's rows is free
+            if (C::S - 1 < nk) issue((ring + C::S - 1) % C::S, C::S - 1);
+            wait_stage(min(C::S - 1, nk - 1));
+            lds_barrier();
+            enter(0);
+#pragma unroll
+            for (int mi = 0; mi < C::MI; ++mi) read_a(0, mi);
+#pragma unroll
+            for (int p = 0; p < 3; ++p) read_b(p);
+            read_scales(0);
+            before_turn(std::false_type());
+            const std::integral_constant<int, kTurn> from_turn;
+            const std::integer_sequence<int, 0, 1> two;
+            for (int kt = 0; kt + 1 < nk; ++kt) {
+                // Scales of two slices went out in the turn of each odd step, before its
+                // slice: they are younger than slice kt + 1 in even steps.
+                wait_stage(min(C::S - 2, nk - 2 - kt), C::S > 2 && kt > 0 && !(kt & 1) && kt / 2 + 1 < nchunks ? s_ops : 0);
+                lds_barrier();
+                if ((kt & 1) && (kt + 3) / 2 < nchunks) issue_scales((kt + 3) / 2);
+                fill = kt + C::S;
+                fill_slot = (ring + kt) % C::S;
+                enter(kt + 1);
+                positions(from_turn, two, std::true_type(), std::true_type());
+#pragma unroll
+                for (int mi = 0; mi < C::MI; ++mi) sa[0][mi] = sa[1][mi];
+#pragma unroll
+                for (int ni = 0; ni < C::NI; ++ni) sw[0][ni] = sw[1][ni];
+                before_turn(std::true_type());
             }
+            positions(from_turn, two, std::false_type(), std::false_type());
+        } else for (int kt = 0; kt < nk; ++kt) {
+            wait_stage(min(C::S - 2, nk - 1 - kt));
             lds_barrier();  // slice kt is in LDS for every wave; slot of slice kt-1 is free
-            if constexpr (C::A4) {
-                if (!(kt & 1) && kt / 2 + 1 < nchunks) issue_scales(kt / 2 + 1);
-            }
             if (kt + C::S - 1 < nk) issue((ring + kt + C::S - 1) % C::S, kt + C::S - 1);
             const char* la = lds + ((ring + kt) % C::S) * C::STAGE;
             const char* lb = la + C::A_BYTES;
@@ -854,68 +951,6 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                         acc[mi][ni] += ((MODE == FC1 && (ni & 1)) ? s1[mi] : s0[mi]) * pr[jj % (LAGB + 1)];
                     }
                     __builtin_amdgcn_sched_barrier(0);
-                }
-            } else if constexpr (C::A4) {
-                const int g4 = lane >> 4;
-                const char* ls = lds + C::S * C::STAGE + ((kt >> 1) & 1) * (C::S_OPS * 1024);
-                // bytes 8 (kt % 2) + 2g of a row's sixteen
-                const int pair = (kt & 1) * 8 + g4 * 2;
-                const int at = wide ? pair : (pair >> 2) * 256 + (pair & 3), rs = wide ? 16 : 4;
-                auto scale_at = [&](int row) { return ls + (row >> 6) * 1024 + ((row & 63) + (lane & 15)) * rs + at; };
-                // Software pipeline: a weight fragment is read before the MI products in
-                // front of its own are issued, an activation fragment of the second
-                // K-step behind the last product with the first one's.  (Left to the
-                // compiler every fragment was waited for where it was read: 1031 against
-                // 957 us for 4096 tokens of the Mixtral-shaped layer.)
-                if (half_last && kt == nk - 1) {
-                    // past the rows' end: zeros where groups 2 and 3 read activations
-                    for (int i = tid; i < C::BM * 4; i += C::NT) {
-                        const int row = i >> 2, v = (i & 2) * 2 + 2 + (i & 1);  // virtual chunks 2, 3, 6, 7
-                        *reinterpret_cast<u32x4_t*>(const_cast<char*>(la) + dma_off(row, v)) = u32x4_t{0u, 0u, 0u, 0u};
-                    }
-                    lds_barrier();
-                }
-                {
-                    int sa[C::MI], sw[C::NI];
-                    u32x4_t fa[C::MI], fb[2];
-                    auto read_a = [&](int b, int mi) {
-                        fa[mi] = *reinterpret_cast<const u32x4_t*>(
-                            la + dma_off(wm * C::WTM + mi * 16 + (lane & 15), 4 * b + g4));
-                    };
-                    auto read_b = [&](int b, int ni) {
-                        return *reinterpret_cast<const u32x4_t*>(
-                            lb + dma_off(wn * C::WTN + ni * 16 + (lane & 15), 4 * b + g4));
-                    };
-#pragma unroll
-                    for (int mi = 0; mi < C::MI; ++mi) {
-                        sa[mi] = *reinterpret_cast<const uint16_t*>(scale_at(wm * C::WTM + mi * 16));
-                        read_a(0, mi);
-                    }
-#pragma unroll
-                    for (int ni = 0; ni < C::NI; ++ni)
-                        sw[ni] = *reinterpret_cast<const uint16_t*>(scale_at(C::BM + wn * C::WTN + ni * 16));
-                    fb[0] = read_b(0, 0);
-                    __builtin_amdgcn_sched_barrier(0);
-                    auto kstep = [&](auto step) {
-                        constexpr int b = decltype(step)::value;
-#pragma unroll
-                        for (int ni = 0; ni < C::NI; ++ni) {
-                            const int at = b * C::NI + ni;
-                            if (ni + 1 < C::NI) fb[(at + 1) & 1] = read_b(b, ni + 1);
-                            else if (b == 0) fb[(at + 1) & 1] = read_b(1, 0);
-#pragma unroll
-                            for (int mi = 0; mi < C::MI; ++mi) {
-                                acc[mi][ni] = mfma_mxfp4<b>(fb[at & 1], fa[mi], acc[mi][ni], sw[ni], sa[mi]);
-                                if (b == 0 && ni + 1 == C::NI) {
-                                    __builtin_amdgcn_sched_barrier(0);
-                                    read_a(1, mi);
-                                }
-                            }
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                    };
-                    kstep(std::integral_constant<int, 0>());
-                    kstep(std::integral_constant<int, 1>());
                 }
             } else {
 #pragma unroll
@@ -990,6 +1025,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
 #pragma unroll
                 for (int q = 0; q < C::IPW_S; ++q) ssrc[q] = s_source(nxt, q, nsidx[q]);
                 issue_scales(0);
+                if (nchunks > 1) issue_scales(1);
             }
             ring = (ring + nk) % C::S;
 #pragma unroll
@@ -1004,7 +1040,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
         bf16_t* out = reinterpret_cast<bf16_t*>(a.out);
         const int erow = lane & 15;        // row within a 16x16 block
         const int ecol = (lane >> 4) * 4;  // first of its 4 columns
-        if (MODE == FC1 && C::A8) {
+        if constexpr (MODE == FC1 && C::A8) {
             // h -> e4m3 per row and 128 intermediate channels: the tile's 128 h
             // columns are split over the WN wave columns, 4 lanes per row each
             // (lanes l, l^16, l^32, l^48).  h overwrites the gate accumulators.
@@ -1052,37 +1088,37 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                     if (wn == 0 && lane < 16) static_cast<float*>(a.out_scale)[r * sk_out + cur.nt] = sc;
                 }
             }
-        } else if (MODE == FC1 && C::A4) {
-            // h -> MXFP4 per row and 32 channels: pairs 2b and 2b + 1 of this wave,
-            // eight channels in each of the four lanes that share a row
+        } else if constexpr (MODE == FC1 && C::A4) {
+            // h -> MXFP4 per row and 32 channels: a gate and an up block, sixteen
+            // neighbouring channels in each of the two lanes that share a row
             uint8_t* hq = reinterpret_cast<uint8_t*>(a.out);
             uint8_t* hs = reinterpret_cast<uint8_t*>(a.out_scale);
+            typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 #pragma unroll
             for (int mi = 0; mi < C::MI; ++mi) {
-                const int rr = cur.m0 + wm * C::WTM + mi * 16 + erow;
+                const int rr = cur.m0 + wm * C::WTM + mi * 32 + (lane & 31);
                 const size_t r = (size_t)(cur.row0 + rr);
 #pragma unroll
-                for (int b = 0; b < C::NI / 4; ++b) {
-                    float hv[8];
+                for (int b = 0; b < C::NI / 2; ++b) {
+                    float hv[2][8];
                     uint32_t m = 0;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float gt = acc[mi][4 * b + (i >> 2) * 2][i & 3];
-                        const float up = acc[mi][4 * b + (i >> 2) * 2 + 1][i & 3];
-                        hv[i] = silu_exp2(gt) * up;
-                        m = max(m, __float_as_uint(hv[i]) & 0x7fffffffu);
+                    for (int i = 0; i < 16; ++i) {
+                        const float h = silu_exp2(acc[mi][2 * b][i]) * acc[mi][2 * b + 1][i];
+                        hv[i >> 3][i & 7] = h;
+                        m = max(m, __float_as_uint(h) & 0x7fffffffu);
                     }
-                    m = max_over_groups(m);
-                    const uint32_t sc = mxfp4_scale(m);
+                    const auto both = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+                    const uint32_t sc = mxfp4_scale(max(both[0], both[1]));
                     if (rr < cur.nrows) {
                         const int blk = cur.nt * (C::BN / 64) + wn * (C::WTN / 64) + b;  // of the row's I / 32
-                        *(__attribute__((address_space(1))) uint32_t*)(hq + r * (a.I / 2) + blk * 16 + (lane >> 4) * 4) =
-                            mxfp4_codes(hv, sc);
-                        if (lane < 16) hs[r * (a.I / 32) + blk] = (uint8_t)sc;
+                        *(__attribute__((address_space(1))) u32x2_t*)(hq + r * (a.I / 2) + blk * 16 + (lane >> 5) * 8) =
+                            u32x2_t{mxfp4_codes(hv[0], sc), mxfp4_codes(hv[1], sc)};
+                        if (lane < 32) hs[r * (a.I / 32) + blk] = (uint8_t)sc;
                     }
                 }
             }
-        } else if (MODE == FC1) {
+        } else if constexpr (MODE == FC1) {
 #pragma unroll
             for (int mi = 0; mi < C::MI; ++mi)
 #pragma unroll
@@ -1100,7 +1136,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
                     if (rr < cur.nrows) store4_bf16(out + (size_t)(cur.row0 + rr) * a.out_ld + col, hv);
                 }
         } else {
-            // FC2: each wave stages its output 16 rows at a time (bf16) in its
+            // FC2: each wave stages its output 16 (A4: 32) rows at a time (bf16) in its
             // share of the ring slot that the next tile fills last, then writes
             // whole 16-byte column chunks, 2*WTN contiguous bytes per row, instead
             // of 8-byte pieces scattered over 16 rows per store instruction.  The
@@ -1109,7 +1145,7 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
             constexpr int PITCH = C::WTN * 2 + 16;  // staged row bytes (+16 spreads the banks)
             constexpr int CPR = C::WTN / 8;         // 16-byte chunks per row
             constexpr int RPI = 64 / CPR;           // rows per read / store instruction
-            static_assert(16 * PITCH <= C::STAGE / C::NW && 16 % RPI == 0, "epilogue staging");
+            static_assert(C::MB * PITCH <= C::STAGE / C::NW && C::MB % RPI == 0, "epilogue staging");
             const int fslot = has_next ? (ring + C::S - 1) % C::S : 0;
             char* stg = lds + fslot * C::STAGE + wave * (C::STAGE / C::NW);
 #pragma unroll
@@ -1117,14 +1153,25 @@ __global__ __launch_bounds__(C::NT) void dma_gemm_kernel(FfnArgs a)
 #pragma unroll
                 for (int ni = 0; ni < C::NI; ++ni) {
                     typedef unsigned u32x2_t __attribute__((ext_vector_type(2)));
-                    *reinterpret_cast<u32x2_t*>(stg + erow * PITCH + (ni * 16 + ecol) * 2) =
-                        u32x2_t{pack_bf16x2(acc[mi][ni][0], acc[mi][ni][1]), pack_bf16x2(acc[mi][ni][2], acc[mi][ni][3])};
+                    if constexpr (C::A4) {  // sixteen neighbouring columns
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            u32x4_t v;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                v[q] = pack_bf16x2(acc[mi][ni][8 * i + 2 * q], acc[mi][ni][8 * i + 2 * q + 1]);
+                            *reinterpret_cast<u32x4_t*>(stg + (lane & 31) * PITCH + (ni * 32 + (lane >> 5) * 16 + 8 * i) * 2) = v;
+                        }
+                    } else {
+                        *reinterpret_cast<u32x2_t*>(stg + erow * PITCH + (ni * 16 + ecol) * 2) =
+                            u32x2_t{pack_bf16x2(acc[mi][ni][0], acc[mi][ni][1]), pack_bf16x2(acc[mi][ni][2], acc[mi][ni][3])};
+                    }
                 }
 #pragma unroll
-                for (int j = 0; j < 16 / RPI; ++j) {
+                for (int j = 0; j < C::MB / RPI; ++j) {
                     const int r = j * RPI + lane / CPR, c = lane % CPR;
                     const u32x4_t d = *reinterpret_cast<const u32x4_t*>(stg + r * PITCH + c * 16);
-                    const int rr = cur.m0 + wm * C::WTM + mi * 16 + r;
+                    const int rr = cur.m0 + wm * C::WTM + mi * C::MB + r;
                     // N is a multiple of 16: a 16-byte chunk is wholly inside or outside
                     const int col = cur.nt * C::BN + wn * C::WTN + c * 8;
                     if (rr < cur.nrows && col < a.N)

@@ -76,11 +76,11 @@ def may_be(packed, scale, v, off):
 
 def h_of(x, w13):
     """(h, how far fp32 work may put it off) of rows x and one expert's weights, all in 64 bits.
-    A product sums K terms in K/128 steps, each of them half a step of fp32 of what has been summed;
+    A product sums K terms in K/64 steps, each of them half a step of fp32 of what has been summed;
     SwiGLU's exponential, reciprocal and products are within 8 half-steps together."""
     I = w13.shape[0] // 2
     gu, size = x @ w13.t(), x.abs() @ w13.abs().t()
-    err = (x.shape[1] / 128 + 2) * EPS32 * size
+    err = (x.shape[1] / 64 + 2) * EPS32 * size
     g, u = gu[:, :I], gu[:, I:]
     sig = torch.sigmoid(g)
     h = g * sig * u
@@ -92,4 +92,4 @@ def h_of(x, w13):
 
 def out_of(h, w2):
     """(rows, how far fp32 work may put them off) of given h."""
-    return h @ w2.t(), (h.shape[1] / 128 + 2) * EPS32 * (h.abs() @ w2.abs().t())
+    return h @ w2.t(), (h.shape[1] / 64 + 2) * EPS32 * (h.abs() @ w2.abs().t())

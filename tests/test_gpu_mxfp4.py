@@ -219,6 +219,13 @@ def test_ffn(counts, H, I):
     c.check(*run(c))
 
 
+@pytest.mark.parametrize("H,I", [(2560, 2688), (1792, 2304), (1408, 1536)])
+def test_ffn_long_rows(H, I):
+    """Rings that go round, in each class of tiles: 5.5 to 10.5 stages, scales in one transfer and in four."""
+    case = Case((33, 1, 400, 90), H, I)
+    case.check(*run(case))
+
+
 def test_ffn_shared_and_several_places():
     c = Case((40, 0, 12, 8), 256, 256, n_shared=2, k=3, seed=5)
     c.check(*run(c))
