@@ -591,7 +591,8 @@ moe_status moe_expert_ffn_mxfp4(const uint8_t* xq, const uint8_t* x_scale, int T
 
 /*
  * moe_layer_few -- the whole layer for at most MOE_FEW_MAX_T tokens (a decoding
- * or speculative step), router logits to output, in two kernels:
+ * or speculative step), router logits to output, in two kernels (past eight tokens
+ * three, moe_route's first):
  *     ids, scales = moe_route(logits)
  *     y_t = sum_j scales[t,j] W2_e (silu(W1_e x_t) * (W3_e x_t)),  e = ids[t,j]
  *           + the shared experts' rows

@@ -1,14 +1,17 @@
-// moe_layer_few: the whole layer for at most MOE_FEW_MAX_T tokens in two kernels.
+// moe_layer_few: the whole layer for at most MOE_FEW_MAX_T tokens in two kernels, or
+// three.
 //
 //   FC1   h[r, c] = silu(x_t . W1_e[c]) * (x_t . W3_e[c])   for each (expert, token) pair r
 //   FC2   y[t, n] = sum_j s_tj (h[r_tj] . W2_{e_tj}[n])  (+ shared experts)
 //
 // A few tokens are bound by the weights of the experts that they choose, each read
-// once, and by latency.  So the routing is done inside FC1, by every workgroup for
-// itself (a wave a token, the tables in LDS), and the weighted sum inside FC2,
-// whose workgroups own output columns and walk through all experts: two launches
-// instead of the five or more of the four-call layer, and no row of FC2 goes
-// through memory.  The pairs' rows are numbered as moe_permute numbers them, by
+// once, and by latency.  So the routing of up to eight tokens is done inside FC1, by
+// every workgroup for itself (a wave a token, the tables in LDS), and the weighted sum
+// inside FC2, whose workgroups own output columns and walk through all experts: two
+// launches instead of the five or more of the four-call layer, and no row of FC2 goes
+// through memory.  With more tokens moe_route's kernel goes first, where a wave would
+// have had several to route (32 tokens of H 512, I 512, E 256 with groups: 119 us with
+// four a wave, 105 so).  The pairs' rows are numbered as moe_permute numbers them, by
 // expert and token, then those of the shared experts.
 //
 // A workgroup of eight waves takes 16 columns (of h: 16 gate and 16 up rows of the
@@ -431,40 +434,44 @@ __global__ __launch_bounds__(kThreads) void few_fc1_kernel(FewArgs a, RouteArgs 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
-    // ---- routing of every token, by every workgroup; the last one, which has the
-    // fewest items, writes it out
+    // ---- routing, by every workgroup; the last one, which has the fewest items,
+    // writes it out
     const bool last = blockIdx.x == gridDim.x - 1;
+    const int pairs = a.T * a.k;  // kThreads >= kMaxPairs
     __shared__ int ids[kMaxPairs];
+    const bool routed = a.T > kWaves;  // moe_route's kernel has run: ids and weights are there
     float logit[4], scale = 0.0f;
-    if (wave < a.T) load_logits(ra, wave, lane, logit);
+    int id = 0;
+    if (!routed && wave < a.T) load_logits(ra, wave, lane, logit);
+    if (routed && tid < pairs) {
+        id = a.ids[tid];
+        if (last) scale = a.scales[tid];
+    }
     if (tid < MOE_MAX_EXPERTS) tb.mask[tid] = 0;
     __syncthreads();
-#pragma unroll 1
-    for (int t = wave; t < a.T; t += kWaves) {
-        float more[4];
-        if (t + kWaves < a.T) load_logits(ra, t + kWaves, lane, more);
-        int id;
+    auto enter = [&](int pair, int t) {
+        ids[pair] = id;
+        atomicOr(&tb.mask[id], 1u << t);
+        if (last) plan.weight[pair] = scale;  // by pair until the rows are known
+    };
+    if (routed) {
+        if (tid < pairs) enter(tid, tid / a.k);
+    } else if (wave < a.T) {
         if (last) route_token<true>(ra, logit, lane, lds.route[wave], id, scale);
         else route_token<false>(ra, logit, lane, lds.route[wave], id, scale);
         if (lane < a.k) {
-            ids[t * a.k + lane] = id;
-            atomicOr(&tb.mask[id], 1u << t);
+            enter(wave * a.k + lane, wave);
             if (last) {
-                a.ids[t * a.k + lane] = id;
-                a.scales[t * a.k + lane] = scale;
-                plan.weight[t * a.k + lane] = scale;  // by pair until the rows are known
+                a.ids[wave * a.k + lane] = id;
+                a.scales[wave * a.k + lane] = scale;
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) logit[i] = more[i];
     }
     __syncthreads();
     if (wave == 0) make_chunks(a, tb, plan, lane);
     __syncthreads();
-    const int pairs = a.T * a.k;  // kThreads >= kMaxPairs
-    int row = 0;
     if (tid < pairs) {
-        row = row_of(tb, ids[tid], tid / a.k);
+        const int row = row_of(tb, ids[tid], tid / a.k);
         plan.token[row] = tid / a.k;
         if (last) {
             a.plan->token[row] = tid / a.k;
@@ -661,6 +668,10 @@ moe_status launch_layer_few(const void* x, const float* logits, int T, int H, in
     a.scales = scales;
     a.T = T; a.H = H; a.I = I; a.E = E; a.k = k; a.n_shared = n_shared;
     const RouteArgs ra{logits, bias, T, E, method, k, n_group, topk_group, scaling, flags};
+    if (T > kWaves) {
+        const moe_status st = launch_route(logits, T, E, method, k, n_group, topk_group, bias, scaling, flags, ids, scales, s);
+        if (st != MOE_OK) return st;
+    }
     if (wdt == MOE_F32) return run_few<float>(a, ra, s);
     if (wdt == MOE_BF16) return run_few<bf16_t>(a, ra, s);
     if (wdt == MOE_FP8_E4M3) return run_few<fp8_t>(a, ra, s);

@@ -7,7 +7,7 @@ expert_ffn_fp8.  With fused=True the FFN step is the one-kernel form with h kept
 on chip (expert_ffn_fused / expert_ffn_fp8_fused: same results, no workspace
 for h).  With mxfp4=True (bf16 x, MXFP4 weights) the FFN step is quantize_mxfp4(x)
 followed by expert_ffn_mxfp4.  With few=True (at most FEW_MAX_T tokens, weights of
-any type) the whole layer is one call, layer_few, of two kernels.
+any type) the whole layer is one call, layer_few, of two or three kernels.
 """
 from __future__ import annotations
 
