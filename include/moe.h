@@ -612,13 +612,14 @@ moe_status moe_expert_ffn_mxfp4(const uint8_t* xq, const uint8_t* x_scale, int T
  *  y         device [T, H] out in `act`.
  *  ws        device workspace of moe_layer_few_workspace_size(...) bytes; on
  *            return it holds h [T*k + n_shared*T, I], rows in moe_permute's order,
- *            and the plan that the second kernel reads.
+ *            and then the plan and the sums that FC2 works with.
  * H and I are multiples of 128, at most 2^20; h and one expert's w13 are below
  * 4 GiB (MOE_ERR_UNSUPPORTED).  x, the weights, their scales, y
  * and ws are 16-byte aligned; no output is an input or another output.  The same
  * inputs give the same bits.  ids, scales and h of a token do not depend on the
- * other tokens; y's order of summation does, unless I is a multiple of 1024 (512
- * for fp32 weights, 2048 for MXFP4).
+ * other tokens; y's order of summation does, unless I is a multiple of 1024 n (512 n
+ * for fp32 weights, 2048 n for MXFP4) with n = 8 for H up to 512, 4 up to 1024, 2 up to
+ * 2048, else 1 (n workgroups share columns of y).
  * NaN logits of a token give unspecified values in that token's rows.
  */
 moe_status moe_layer_few(const void* x, int act, const float* logits, int T, int H, int I, int E, int method,

@@ -742,7 +742,7 @@ static moe_status check_few(int T, int H, int I, int E, int k, int n_shared, int
 size_t moe_layer_few_workspace_size(int T, int H, int I, int E, int k, int n_shared, int act)
 {
     if (check_few(T, H, I, E, k, n_shared, act, act) != MOE_OK || T == 0) return 0;
-    return few_scratch_bytes(T, I, k, n_shared, act);
+    return few_scratch_bytes(T, H, I, k, n_shared, act);
 }
 
 moe_status moe_layer_few(const void* x, int act, const float* logits, int T, int H, int I, int E, int method,
@@ -771,7 +771,7 @@ moe_status moe_layer_few(const void* x, int act, const float* logits, int T, int
         return same_buffer();
     if (!aligned16({x, w13, w2, w13_scale, w2_scale, y, ws}))
         return set_error(MOE_ERR_INVALID_ARG, "x, the weights, their scales, y and the workspace must be 16-byte aligned");
-    const size_t need = few_scratch_bytes(T, I, k, n_shared, act);
+    const size_t need = few_scratch_bytes(T, H, I, k, n_shared, act);
     if (!ws || ws_bytes < need)
         return set_error(MOE_ERR_WORKSPACE, "layer_few needs %zu workspace bytes (got %zu)", need, ws_bytes);
     return launch_layer_few(x, logits, T, H, I, E, method, k, n_group, topk_group, bias, scaling, flags, n_shared,

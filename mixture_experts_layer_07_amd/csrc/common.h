@@ -138,7 +138,7 @@ moe_status launch_quantize_mxfp4(const void* x, int dt, int rows, int cols, uint
                                  hipStream_t s);
 moe_status launch_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int rows, int cols, int dt, void* x,
                                    hipStream_t s);
-size_t few_scratch_bytes(int T, int I, int k, int n_shared, int act);
+size_t few_scratch_bytes(int T, int H, int I, int k, int n_shared, int act);
 moe_status launch_layer_few(const void* x, const float* logits, int T, int H, int I, int E, int method, int k,
                             int n_group, int topk_group, const float* bias, float scaling, unsigned flags,
                             int n_shared, const void* w13, const void* w2, int wdt, const void* w13_scale,

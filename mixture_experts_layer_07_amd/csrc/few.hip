@@ -72,6 +72,9 @@ struct FewArgs {
     int32_t* ids;       // [T, k]
     float* scales;
     int T, H, I, E, k, n_shared;
+    int splits;         // workgroups that share a column tile of FC2
+    float* part;        // ... [H/16, splits, T, 16] their sums, if more than one
+    int* arrived;       // [H/16] how many of them are there
 };
 
 // ---------------------------------------------------------------- tables
@@ -480,6 +483,8 @@ __global__ __launch_bounds__(kThreads) void few_fc1_kernel(FewArgs a, RouteArgs 
     }
     __syncthreads();
     if (last) {
+        if (a.splits > 1)
+            for (int i = tid; i < a.H / 16; i += kThreads) a.arrived[i] = 0;
         for (int i = tid; i < plan.nchunks; i += kThreads) a.plan->chunk[i] = plan.chunk[i];
         if (tid == 0) {
             a.plan->nchunks = plan.nchunks;
@@ -496,18 +501,24 @@ __global__ __launch_bounds__(kThreads) void few_fc1_kernel(FewArgs a, RouteArgs 
 typedef f32x4_t Columns[kWaves][MOE_FEW_MAX_T][4];  // each wave's sums: 16 columns a token
 
 // The column tiles of this workgroup.  A wave's pieces are every eighth of all
-// (chunk, piece) pairs; the loads run ahead as in FC1, within a tile.
+// (chunk, piece) pairs; the loads run ahead as in FC1, within a tile.  Where there are
+// fewer tiles than CUs, a.splits workgroups share one, and its pieces: each leaves its
+// sums in the workspace, and the last to arrive adds them up, in the workgroups' order
+// (32 bf16 tokens: H 2048, I 1024, E 64 159 -> 142 us for the layer, H 512, I 512, E 256
+// 106 -> 60).
 template <class WT, bool MANY>
 __device__ __forceinline__ void fc2_tiles(const FewArgs& a, const Plan& plan, Columns& ys, char* stage, int wave, int lane)
 {
     using F = Form<WT>;
     using act = typename F::act;
     using P = Piece<WT, 1, MANY>;
-    const int np = (a.I + F::kPE - 1) / F::kPE, all = __builtin_amdgcn_readfirstlane(plan.nchunks) * np, tiles = a.H / 16;
+    const int np = (a.I + F::kPE - 1) / F::kPE, all = __builtin_amdgcn_readfirstlane(plan.nchunks) * np;
+    const int items = a.H / 16 * a.splits, waves = kWaves * a.splits;
     const bool ragged = a.I % F::kPE != 0;
     const uint32_t ld = F::bytes(a.I), woff = (lane >> 3) * ld + (lane & 7) * 16;
     const int g = lane >> 4;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+        const int tile = item / a.splits, split = item % a.splits, first = split * kWaves + wave;
         for (int i = lane; i < a.T * 4; i += 64) ys[wave][i >> 2][i & 3] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         struct Loads {
             int chunk, p, e, row[1];
@@ -534,22 +545,22 @@ __device__ __forceinline__ void fc2_tiles(const FewArgs& a, const Plan& plan, Co
             r.load_scales(a.s2, ahead.e, a.H, a.I, ahead.row, ahead.p, lane, half, ahead.valid);
             if (!ahead.valid) return;
             int chunk = ahead.chunk;
-            ahead.p += kWaves;
+            ahead.p += waves;
             while (ahead.p >= np) {
                 ahead.p -= np;
                 ++chunk;
             }
             if (chunk != ahead.chunk) enter(chunk);
         };
-        int chunk = wave / np, p = wave - chunk * np, q = wave;
+        int chunk = first / np, p = first - chunk * np, q = first;
         f32x4_t acc[1] = {{0.f, 0.f, 0.f, 0.f}};
         if (q < all) {
             Chunk c = get_chunk(plan, chunk);
             auto one = [&](const P& r, P& next) {
                 fetch(next);
                 r.add(acc, stage, lane, c.n, F::kHalves && ragged && p == np - 1);
-                q += kWaves;
-                p += kWaves;
+                q += waves;
+                p += waves;
                 if (p < np && q < all) return true;
                 // the wave's last piece of this chunk: its rows to their tokens
                 const int n = lane & 15, row = c.row0 + n;
@@ -571,13 +582,32 @@ __device__ __forceinline__ void fc2_tiles(const FewArgs& a, const Plan& plan, Co
             run_pipeline(buf, fetch, one);
         }
         __syncthreads();
-        for (int i = wave * 64 + lane; i < a.T * 16; i += kThreads) {
-            const int t = i >> 4, col = i & 15;
-            float v = 0.0f;
+        static_assert(MOE_FEW_MAX_T * 16 <= kThreads);
+        const int i = wave * 64 + lane, t = i >> 4, col = i & 15;
+        float v = 0.0f;
+        if (t < a.T) {
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) v += reinterpret_cast<const float*>(&ys[w][t][0])[col];
-            put(reinterpret_cast<act*>(a.y) + (size_t)t * a.H + tile * 16 + col, v);
         }
+        bool writes = t < a.T;
+        if (a.splits > 1) {
+            __shared__ int before;
+            float* part = a.part + (size_t)tile * a.splits * a.T * 16 + i;
+            // Stores and loads that go past the XCD's own L2, the stores complete before
+            // the count goes up: a release fence would write that L2 back (35 us and more).
+            if (writes) __hip_atomic_store(part + split * a.T * 16, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (i == 0) before = __hip_atomic_fetch_add(a.arrived + tile, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            __syncthreads();
+            writes = writes && before == a.splits - 1;
+            if (writes) {
+                v = 0.0f;
+                for (int s = 0; s < a.splits; ++s)
+                    v += __hip_atomic_load(part + s * a.T * 16, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+        if (writes) put(reinterpret_cast<act*>(a.y) + (size_t)t * a.H + tile * 16 + col, v);
         __syncthreads();
     }
 }
@@ -617,7 +647,7 @@ moe_status run_few(const FewArgs& a, const RouteArgs& ra, hipStream_t s)
     }();
     const long cus = device_cu_count(), per = (a.T + 15) / 16;
     const long chunks = std::min((long)a.T * a.k, (long)a.E * per) + a.n_shared * per;  // at most
-    const long g1 = std::min(chunks * (a.I / 16), cus * occ1), g2 = std::min((long)a.H / 16, cus * occ2);
+    const long g1 = std::min(chunks * (a.I / 16), cus * occ1), g2 = std::min((long)a.H / 16 * a.splits, cus * occ2);
     {
         TimedLaunch tl(MOE_KID_FEW_FC1, s);
         hipLaunchKernelGGL((few_fc1_kernel<WT, MAYBE>), dim3((unsigned)g1), dim3(kThreads), 0, s, a, ra);
@@ -637,17 +667,32 @@ moe_status run_few(const FewArgs& a, const RouteArgs& ra, hipStream_t s)
     return a.T <= kFew ? run_few<WT, false>(a, ra, s) : run_few<WT, true>(a, ra, s);
 }
 
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
 size_t few_h_bytes(int T, int I, int k, int n_shared, int act)
 {
     const size_t n = (size_t)T * (k + n_shared) * I * (act == MOE_F32 ? 4 : 2);
-    return (n + 255) & ~(size_t)255;
+    return align256(n);
+}
+
+// Workgroups for a column tile of FC2: by H alone, so that a token's sums have the
+// same order whatever else is in the call.  (kCus stands for the card's CUs also where
+// no device is asked: the workspace's size.)
+int few_splits(int H)
+{
+    constexpr int kCus = 256, kMost = 8;
+    int n = 1;
+    while (n < kMost && H / 16 * n * 2 <= kCus) n *= 2;
+    return n;
 }
 
 }  // namespace
 
-size_t few_scratch_bytes(int T, int I, int k, int n_shared, int act)
+size_t few_scratch_bytes(int T, int H, int I, int k, int n_shared, int act)
 {
-    return few_h_bytes(T, I, k, n_shared, act) + sizeof(Plan);
+    const int splits = few_splits(H);
+    return few_h_bytes(T, I, k, n_shared, act) + align256(sizeof(Plan)) +
+           (splits > 1 ? align256((size_t)H / 16 * 4) + (size_t)splits * T * H * 4 : 0);
 }
 
 moe_status launch_layer_few(const void* x, const float* logits, int T, int H, int I, int E, int method, int k,
@@ -663,6 +708,9 @@ moe_status launch_layer_few(const void* x, const float* logits, int T, int H, in
     a.s2 = w2_scale;
     a.h = static_cast<char*>(ws);
     a.plan = reinterpret_cast<Plan*>(a.h + few_h_bytes(T, I, k, n_shared, wdt == MOE_F32 ? MOE_F32 : MOE_BF16));
+    a.splits = few_splits(H);
+    a.arrived = reinterpret_cast<int*>(reinterpret_cast<char*>(a.plan) + align256(sizeof(Plan)));
+    a.part = reinterpret_cast<float*>(reinterpret_cast<char*>(a.arrived) + align256((size_t)H / 16 * 4));
     a.y = static_cast<char*>(y);
     a.ids = ids;
     a.scales = scales;
