@@ -1264,7 +1264,7 @@ constexpr int kHandoffMinK = 4096;  // remainder hand-off between classes from t
 // measured and is not used: a 32-row tile streams the weights again with a
 // quarter of the waves (fp8 x fp8 Qwen3-shaped FC1 +13%).
 template <int MODE, class Skinny, class Mid, class Big>
-moe_status run_classes_dma(const FfnArgs& f, int R, hipStream_t s, int kid)
+moe_status run_classes_dma(const FfnArgs& f, int R, hipStream_t s, int kid, int big_rows = kBigRows)
 {
     static_assert(Skinny::BM < Mid::BM && Mid::BM <= Big::BM, "tile heights grow with the class");
     // Only for long K: a tile's fixed costs (ring fill, epilogue) are then small
@@ -1275,10 +1275,10 @@ moe_status run_classes_dma(const FfnArgs& f, int R, hipStream_t s, int kid)
     const int big_give = (handoff && Big::BM > Mid::BM) ? Mid::BM : 0;  // none when the shapes match
     moe_status st = run_dma_gemm<MODE, Skinny>(f, 0, kMidRows, R, s, kid);
     if (st != MOE_OK) return st;
-    st = run_dma_gemm<MODE, Mid>(f, kMidRows, kBigRows, R, s, kid, 0, kBigRows, kAllRows, Big::BM,
+    st = run_dma_gemm<MODE, Mid>(f, kMidRows, big_rows, R, s, kid, 0, big_rows, kAllRows, Big::BM,
                                  big_give);
     if (st != MOE_OK) return st;
-    return run_dma_gemm<MODE, Big>(f, kBigRows, kAllRows, R, s, kid, big_give);
+    return run_dma_gemm<MODE, Big>(f, big_rows, kAllRows, R, s, kid, big_give);
 }
 
 // Shapes chosen by measurement on MI355X: 4 waves per SIMD for the large tiles
@@ -1333,13 +1333,20 @@ moe_status run_classes_a8(const FfnArgs& f, int R, hipStream_t s, int kid)
                            DmaCfg<256, 256, 4, 2, 4, 2, true, true>>(f, R, s, kid);
 }
 
-// MXFP4 activations and weights.
+// MXFP4 activations and weights.  A 256x256 tile takes 1.35 times a 128x256 one, so
+// groups past 128 rows take it where such groups are many: 8192 tokens of the
+// DeepSeek-V3-shaped layer (256 rows a group) 2680 -> 2547 us, 2048 tokens of H 4096,
+// I 2048, E 128 (128 rows) 579 -> 560.  Where they are few, their launch would not fill
+// the chip: 512 tokens of the first layer (16 rows a group) 1069 -> 1146 us, 1024 tokens
+// 1186 -> 1213, 1000 rows of a small layer 44 -> 59.
 template <int MODE>
 moe_status run_classes_a4(const FfnArgs& f, int R, hipStream_t s, int kid)
 {
+    const long tiles = (long)(R / 256) * (f.N / 256);
+    const int big_rows = R / f.G >= 128 && tiles >= 512 ? 129 : kBigRows;
     return run_classes_dma<MODE, DmaCfg<32, 256, 1, 4, 2, 4, false, false, true>,
                            DmaCfg<128, 256, 2, 4, 2, 3, false, false, true>,
-                           DmaCfg<256, 256, 2, 4, 4, 2, false, false, true>>(f, R, s, kid);
+                           DmaCfg<256, 256, 2, 4, 4, 2, false, false, true>>(f, R, s, kid, big_rows);
 }
 
 // fp32 (small reference-precision layers): one 32x128 tile shape for all groups.

@@ -238,6 +238,13 @@ def test_ffn_class_borders(n):
     c.check(*run(c))
 
 
+@pytest.mark.parametrize("H,I", [(128, 2048), (4096, 128)])
+def test_ffn_many_rows(H, I):
+    """Enough of them that groups past 128 rows take the largest tiles, in FC1 and in FC2."""
+    case = Case((64, 128, 129, 200, 256, 257, 300, 383, 384, 700, 33, 5400), H, I)
+    case.check(*run(case))
+
+
 @pytest.mark.parametrize("n", [400, 513, 640])
 def test_ffn_hand_off(n):
     """Long rows: a big group's remainder goes to the smaller tiles, in FC1 and in FC2."""
