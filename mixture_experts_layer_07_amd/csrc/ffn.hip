@@ -1264,7 +1264,8 @@ constexpr int kHandoffMinK = 4096;  // remainder hand-off between classes from t
 // measured and is not used: a 32-row tile streams the weights again with a
 // quarter of the waves (fp8 x fp8 Qwen3-shaped FC1 +13%).
 template <int MODE, class Skinny, class Mid, class Big>
-moe_status run_classes_dma(const FfnArgs& f, int R, hipStream_t s, int kid, int big_rows = kBigRows)
+moe_status run_classes_dma(const FfnArgs& f, int R, hipStream_t s, int kid, int big_rows = kBigRows,
+                           int most = kAllRows)  // no group has more rows
 {
     static_assert(Skinny::BM < Mid::BM && Mid::BM <= Big::BM, "tile heights grow with the class");
     // Only for long K: a tile's fixed costs (ring fill, epilogue) are then small
@@ -1274,10 +1275,10 @@ moe_status run_classes_dma(const FfnArgs& f, int R, hipStream_t s, int kid, int 
     const bool handoff = f.K >= kHandoffMinK;
     const int big_give = (handoff && Big::BM > Mid::BM) ? Mid::BM : 0;  // none when the shapes match
     moe_status st = run_dma_gemm<MODE, Skinny>(f, 0, kMidRows, R, s, kid);
-    if (st != MOE_OK) return st;
+    if (st != MOE_OK || most < kMidRows) return st;
     st = run_dma_gemm<MODE, Mid>(f, kMidRows, big_rows, R, s, kid, 0, big_rows, kAllRows, Big::BM,
                                  big_give);
-    if (st != MOE_OK) return st;
+    if (st != MOE_OK || most < big_rows) return st;
     return run_dma_gemm<MODE, Big>(f, big_rows, kAllRows, R, s, kid, big_give);
 }
 
@@ -1344,9 +1345,10 @@ moe_status run_classes_a4(const FfnArgs& f, int R, hipStream_t s, int kid)
 {
     const long tiles = (long)(R / 256) * (f.N / 256);
     const int big_rows = R / f.G >= 128 && tiles >= 512 ? 129 : kBigRows;
+    const int most = f.T * f.k;  // a class that no group can be of is not launched (2 to 4 us)
     return run_classes_dma<MODE, DmaCfg<32, 256, 1, 4, 2, 4, false, false, true>,
                            DmaCfg<128, 256, 2, 4, 2, 3, false, false, true>,
-                           DmaCfg<256, 256, 2, 4, 4, 2, false, false, true>>(f, R, s, kid, big_rows);
+                           DmaCfg<256, 256, 2, 4, 4, 2, false, false, true>>(f, R, s, kid, big_rows, most);
 }
 
 // fp32 (small reference-precision layers): one 32x128 tile shape for all groups.
