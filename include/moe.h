@@ -15,7 +15,11 @@
  * With fp8 activations the FFN step is moe_quantize_fp8 (of x) followed by
  * moe_expert_ffn_fp8; route, permute and finalize are unchanged.  The FFN step
  * can also run as one kernel that keeps h on chip (moe_expert_ffn_fused,
- * moe_expert_ffn_fp8_fused; same results, no workspace).
+ * moe_expert_ffn_fp8_fused; same results, no workspace).  With 4-bit activations
+ * and weights (OCP MXFP4) it is moe_quantize_mxfp4 followed by
+ * moe_expert_ffn_mxfp4; moe_dequantize_mxfp4 gives the codes' values.  For at most
+ * MOE_FEW_MAX_T tokens moe_layer_few is the whole layer in one call, with weights of
+ * any of these types.
  *
  * Around the experts' matrix products the library also has the layer's row
  * operators, for serving and for training with a caller's own products:
