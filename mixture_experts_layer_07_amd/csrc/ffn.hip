@@ -1339,15 +1339,21 @@ moe_status run_classes_a8(const FfnArgs& f, int R, hipStream_t s, int kid)
 // DeepSeek-V3-shaped layer (256 rows a group) 2680 -> 2547 us, 2048 tokens of H 4096,
 // I 2048, E 128 (128 rows) 579 -> 560.  Where they are few, their launch would not fill
 // the chip: 512 tokens of the first layer (16 rows a group) 1069 -> 1146 us, 1024 tokens
-// 1186 -> 1213, 1000 rows of a small layer 44 -> 59.
+// 1186 -> 1213.
 template <int MODE>
 moe_status run_classes_a4(const FfnArgs& f, int R, hipStream_t s, int kid)
 {
     const long tiles = (long)(R / 256) * (f.N / 256);
     const int big_rows = R / f.G >= 128 && tiles >= 512 ? 129 : kBigRows;
     const int most = f.T * f.k;  // a class that no group can be of is not launched (2 to 4 us)
-    return run_classes_dma<MODE, DmaCfg<32, 256, 1, 4, 2, 4, false, false, true>,
-                           DmaCfg<128, 256, 2, 4, 2, 3, false, false, true>,
+    using Mid = DmaCfg<128, 256, 2, 4, 2, 3, false, false, true>;
+    // Where the tiles of all groups are one round of the chip, one launch of them: 333
+    // tokens of H 384, I 640, E 12, k 3 44 -> 22 us, 64 of H 2048, I 1408, E 8, k 2 52 -> 29,
+    // 200 of H 7168, I 256, E 32, k 4 90 -> 62 (but 64 of H 4096, I 2048, E 4, whose groups
+    // are all of the first class, 35 -> 39).
+    if (most >= kMidRows && (long)(R / Mid::BM + f.G) * ((f.N + Mid::BN - 1) / Mid::BN) <= device_cu_count())
+        return run_dma_gemm<MODE, Mid>(f, 0, kAllRows, R, s, kid);
+    return run_classes_dma<MODE, DmaCfg<32, 256, 1, 4, 2, 4, false, false, true>, Mid,
                            DmaCfg<256, 256, 2, 4, 4, 2, false, false, true>>(f, R, s, kid, big_rows, most);
 }
 

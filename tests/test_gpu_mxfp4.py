@@ -143,7 +143,7 @@ def test_empty_and_refusals():
 class Case:
     """Inputs of one call, on the host in 64 bits and on the GPU."""
 
-    def __init__(self, counts, H, I, n_shared=0, T=None, seed=0, k=None):
+    def __init__(self, counts, H, I, n_shared=0, T=None, seed=0, k=None, alike=False):
         E = len(counts)
         P = sum(counts)
         rng = np.random.default_rng([seed, H, I, E, P])
@@ -160,7 +160,9 @@ class Case:
         self.offsets = torch.from_numpy(np.concatenate(
             [[0], np.cumsum(counts), P + T * np.arange(1, n_shared + 1)]).astype(np.int32))
         G = E + n_shared
-        q = lambda rows, cols, sd: [t.reshape(G, rows, -1) for t in self._weights(G * rows, cols, sd)]  # noqa: E731
+        n = 1 if alike else G  # alike: every expert has the same weights
+        q = lambda rows, cols, sd: [t.reshape(n, rows, -1).expand(G, -1, -1).contiguous()  # noqa: E731
+                                    for t in self._weights(n * rows, cols, sd)]
         (self.w13, self.s13), (self.w2, self.s2) = q(2 * I, H, seed + 1), q(H, I, seed + 2)
         self.R = P + n_shared * T
         xc, xs = ref.encode(self.x)
@@ -242,6 +244,16 @@ def test_ffn_class_borders(n):
 def test_ffn_many_rows(H, I):
     """Enough of them that groups past 128 rows take the largest tiles, in FC1 and in FC2."""
     case = Case((64, 128, 129, 200, 256, 257, 300, 383, 384, 700, 33, 5400), H, I)
+    case.check(*run(case))
+
+
+@pytest.mark.parametrize("H,I,E", [(256, 256, 256), (4096, 1152, 40), (1152, 4096, 70), (2688, 1408, 40)])
+def test_ffn_classes(H, I, E):
+    """Every class of tiles, its borders and the rows it hands on, in a call of more tiles than one
+    round of the chip (which has them all alike)."""
+    counts = [63, 64, 65, 127, 128, 129, 255, 256, 257, 383, 384, 385, 400, 513, 640, 1, 2, 31]
+    counts = np.random.default_rng(E).permutation(counts + [0] * (E - len(counts))).tolist()
+    case = Case(counts, H, I, alike=True)
     case.check(*run(case))
 
 
