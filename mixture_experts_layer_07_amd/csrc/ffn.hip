@@ -31,13 +31,14 @@
 //          16-byte fragment (lane group q feeds K = 4q + i to the i-th MFMA,
 //          the same for A and B, so the four products cover the 16 K values
 //          once).
-//   Direct-to-LDS engine (bf16 activations with bf16 or fp8 weights, or
-//          fp8 activations with fp8 weights): described at DmaCfg below;
-//          v_mfma_f32_16x16x32_bf16, a lane feeding 8 consecutive K values
-//          of one row of A and of B, or v_mfma_f32_16x16x128_f8f6f4 with 32.
+//   Direct-to-LDS engine (bf16 activations with bf16 or fp8 weights, fp8
+//          activations with fp8 weights, or MXFP4 of both): described at DmaCfg
+//          below; v_mfma_f32_16x16x32_bf16, a lane feeding 8 consecutive K values
+//          of one row of A and of B, or v_mfma_f32_16x16x128_f8f6f4 (MXFP4:
+//          32x32x64) with 32.
 // FC1 keeps the gate and up halves of an output column in the same lane: the
-// staged B tile alternates 16 gate rows and the matching 16 up rows, so MFMA
-// column blocks 2q and 2q+1 are gate and up of the same 16 outputs and the
+// staged B tile alternates 16 (MXFP4: 32) gate rows and the matching up rows, so
+// MFMA column blocks 2q and 2q+1 are gate and up of the same outputs and the
 // SwiGLU epilogue needs no data exchange.
 #include <math.h>
 

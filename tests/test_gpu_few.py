@@ -336,6 +336,26 @@ def test_workgroups_that_share_columns(H):
         same(moe.layer_few(**g, ws=ws)[0], want, f"run {i}")
 
 
+def test_two_streams_at_once():
+    """Calls that overlap, each with a workspace of its own."""
+    layers = [Layer(20, 512, 384, 24, 4, "bf16", 1, seed=1), Layer(3, 256, 512, 16, 2, "mxfp4", 0, seed=2)]
+    ins = [a.gpu() for a in layers]
+    want = [moe.layer_few(**i) for i in ins]
+    ws = [moe.layer_few_workspace(a.T, a.H, a.I, a.E, a.k, a.sh, a.dt) for a in layers]
+    streams = [torch.cuda.Stream() for _ in layers]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(50):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(moe.layer_few(**ins[i], ws=ws[i]))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        for out in g:
+            for p, q in zip(out, w):
+                same(p, q, "the streams")
+
+
 def test_large_weights():
     """Experts past 2^32 bytes into the weights."""
     g = torch.Generator(device=DEV).manual_seed(0)
