@@ -582,6 +582,8 @@ def swiglu_backward(dh, guq, gu_scale, want_h=False, out=None):
 # ------------------------------------------------------------------- MXFP4
 # Codes are torch.float4_e2m1fn_x2 [.., cols/2] (two a byte, the even column low) and scales
 # torch.float8_e8m0fnu [.., cols/32]; bytes of a checkpoint become them by .view(dtype).
+# These calls, and layer_few, have no gradient: they warn (UserWarning) of a tensor that requires grad
+# while gradients are enabled.
 _CODES, _SCALES = torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
 
 

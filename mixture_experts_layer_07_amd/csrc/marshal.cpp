@@ -35,10 +35,15 @@ PyObject* g_set_device = nullptr;
 PyObject* g_stream = nullptr;
 
 // ------------------------------------------------------------------- call
+// What a call says of a tensor that requires grad: nothing, or what to do instead.
+const char* const kSilent = nullptr;
+const char* const kBackwardCall = "detach it or call under torch.no_grad(), and use the backward call";  // it has one
+const char* const kNoGradient = "detach it or call under torch.no_grad()";
+
 struct Call {
     const char* name;
-    long index;    // device
-    bool forward;  // a row operator that has a backward call of its own
+    long index;          // device
+    const char* instead;
 };
 
 bool convert(PyObject* o, const Call& c, void** out)
@@ -54,10 +59,9 @@ bool convert(PyObject* o, const Call& c, void** out)
     const at::Tensor& t = THPVariable_Unpack(o);
     // A result that autograd takes for a constant must not lose the caller's gradient without a word.
     // (The gradients' calls may well take such tensors: a caller's own products under autograd.)
-    if (c.forward && t.requires_grad() && c10::GradMode::is_enabled()) {
-        const std::string text = std::string(c.name) +
-                                 ": a tensor requires grad, but the call records no graph; detach it or call under "
-                                 "torch.no_grad(), and use the backward call";
+    if (c.instead && t.requires_grad() && c10::GradMode::is_enabled()) {
+        const std::string text =
+            std::string(c.name) + ": a tensor requires grad, but the call records no graph; " + c.instead;
         if (PyErr_WarnEx(PyExc_UserWarning, text.c_str(), 3)) return false;  // warnings may be errors
     }
     if (!t.is_cuda() || t.device().index() != c.index) {
@@ -157,41 +161,41 @@ int run_any(moe_status (*f)(A...), const Call& c, PyObject* const* args, Py_ssiz
 struct Entry {
     const char* name;
     int (*run)(void*, const Call&, PyObject* const*, Py_ssize_t);
-    bool forward;
+    const char* instead;
     void* address;
 };
 
-#define MOE_ENTRY(fn, forward)                                                                               \
+#define MOE_ENTRY(fn, instead)                                                                           \
     {                                                                                                    \
         #fn,                                                                                             \
             [](void* f, const Call& c, PyObject* const* a, Py_ssize_t n) {                               \
                 return run_any(reinterpret_cast<decltype(&fn)>(f), c, a, n);                             \
             },                                                                                           \
-            forward, nullptr                                                                             \
+            instead, nullptr                                                                             \
     }
 
 Entry g_entries[] = {
-    MOE_ENTRY(moe_route, false),
-    MOE_ENTRY(moe_permute, false),
-    MOE_ENTRY(moe_expert_ffn, false),
-    MOE_ENTRY(moe_expert_ffn_noalloc, false),
-    MOE_ENTRY(moe_expert_ffn_fp8, false),
-    MOE_ENTRY(moe_expert_ffn_fused, false),
-    MOE_ENTRY(moe_expert_ffn_fp8_fused, false),
-    MOE_ENTRY(moe_finalize, false),
-    MOE_ENTRY(moe_quantize_fp8, false),
-    MOE_ENTRY(moe_rmsnorm, true),
-    MOE_ENTRY(moe_rmsnorm_backward, false),
-    MOE_ENTRY(moe_dispatch, true),
-    MOE_ENTRY(moe_dispatch_backward, false),
-    MOE_ENTRY(moe_finalize_backward, false),
-    MOE_ENTRY(moe_route_backward, false),
-    MOE_ENTRY(moe_swiglu, true),
-    MOE_ENTRY(moe_swiglu_backward, false),
-    MOE_ENTRY(moe_quantize_mxfp4, false),
-    MOE_ENTRY(moe_dequantize_mxfp4, false),
-    MOE_ENTRY(moe_expert_ffn_mxfp4, false),
-    MOE_ENTRY(moe_layer_few, false),
+    MOE_ENTRY(moe_route, kSilent),
+    MOE_ENTRY(moe_permute, kSilent),
+    MOE_ENTRY(moe_expert_ffn, kSilent),
+    MOE_ENTRY(moe_expert_ffn_noalloc, kSilent),
+    MOE_ENTRY(moe_expert_ffn_fp8, kSilent),
+    MOE_ENTRY(moe_expert_ffn_fused, kSilent),
+    MOE_ENTRY(moe_expert_ffn_fp8_fused, kSilent),
+    MOE_ENTRY(moe_finalize, kSilent),
+    MOE_ENTRY(moe_quantize_fp8, kSilent),
+    MOE_ENTRY(moe_rmsnorm, kBackwardCall),
+    MOE_ENTRY(moe_rmsnorm_backward, kSilent),
+    MOE_ENTRY(moe_dispatch, kBackwardCall),
+    MOE_ENTRY(moe_dispatch_backward, kSilent),
+    MOE_ENTRY(moe_finalize_backward, kSilent),
+    MOE_ENTRY(moe_route_backward, kSilent),
+    MOE_ENTRY(moe_swiglu, kBackwardCall),
+    MOE_ENTRY(moe_swiglu_backward, kSilent),
+    MOE_ENTRY(moe_quantize_mxfp4, kNoGradient),
+    MOE_ENTRY(moe_dequantize_mxfp4, kNoGradient),
+    MOE_ENTRY(moe_expert_ffn_mxfp4, kNoGradient),
+    MOE_ENTRY(moe_layer_few, kNoGradient),
 };
 
 // A tensor without storage of its own makes torch throw: no exception leaves
@@ -229,7 +233,7 @@ PyObject* call_(PyObject* const* args, Py_ssize_t n)
         if (PyErr_Occurred()) return nullptr;
         entry->address = reinterpret_cast<void*>(a);
     }
-    const int st = entry->run(entry->address, Call{entry->name, dev.has_index() ? (long)dev.index() : -1, entry->forward},
+    const int st = entry->run(entry->address, Call{entry->name, dev.has_index() ? (long)dev.index() : -1, entry->instead},
                               args + 2, n - 2);
     if (st < 0) return nullptr;
     if (st != MOE_OK) {
