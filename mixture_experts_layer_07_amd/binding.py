@@ -32,8 +32,11 @@ FUSED_MAX_I = 2048
 NOALLOC_SCRATCH_BYTES = 64 << 20
 FEW_MAX_T = 32
 
-_DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3,
-       torch.float4_e2m1fn_x2: MXFP4}
+# The 4-bit types; None in a torch that has none of these names.
+_CODES, _SCALES = getattr(torch, "float4_e2m1fn_x2", None), getattr(torch, "float8_e8m0fnu", None)
+_DT = {torch.float32: F32, torch.bfloat16: BF16, torch.float8_e4m3fn: FP8_E4M3}
+if _CODES is not None:
+    _DT[_CODES] = MXFP4
 _lib = None
 _marshal = None
 _loading = threading.Lock()
@@ -584,12 +587,16 @@ def swiglu_backward(dh, guq, gu_scale, want_h=False, out=None):
 # torch.float8_e8m0fnu [.., cols/32]; bytes of a checkpoint become them by .view(dtype).
 # These calls, and layer_few, have no gradient: they warn (UserWarning) of a tensor that requires grad
 # while gradients are enabled.
-_CODES, _SCALES = torch.float4_e2m1fn_x2, torch.float8_e8m0fnu
+def need_mxfp4_types():
+    """Refuses where torch lacks the types of codes or scales."""
+    if _CODES is None or _SCALES is None:
+        raise NotImplementedError("MXFP4 needs a torch with float4_e2m1fn_x2 and float8_e8m0fnu")
 
 
 def quantize_mxfp4(x, out=None):
     """moe_quantize_mxfp4 -> (codes float4_e2m1fn_x2 [rows, cols/2], scale float8_e8m0fnu
     [rows, cols/32]) of x [rows, cols]; weights [.., N, K] go as x.view(-1, K)."""
+    need_mxfp4_types()
     rows, cols = _rows_of(x, "x", _ACT)
     q, scale = (None, None) if out is None else out
     q = _out(q, "codes", (rows, cols // 2), _CODES, x.device)
@@ -600,6 +607,7 @@ def quantize_mxfp4(x, out=None):
 
 def dequantize_mxfp4(codes, scale, dtype=torch.bfloat16, out=None):
     """moe_dequantize_mxfp4 -> the values [rows, cols] of quantize_mxfp4's codes and scales."""
+    need_mxfp4_types()
     rows, half = _rows_of(codes, "codes", _CODES)
     if half % 16:
         raise ValueError(f"codes must be [rows, cols/2] with cols a multiple of 32 (got {tuple(codes.shape)})")
@@ -615,6 +623,7 @@ def expert_ffn_mxfp4(xq, x_scale, expert_offsets, permuted_pair, w13, w2, w13_sc
                      n_shared=0, ws=None, out=None):
     """moe_expert_ffn_mxfp4 -> fc2_out bf16 [T*k + n_shared*T, H]; w13 [G, 2I, H/2] and w2 [G, H, I/2]
     codes with scales [G, 2I, H/32] and [G, H, I/32]."""
+    need_mxfp4_types()
     T, half = _rows_of(xq, "xq", _CODES)
     H, G, d = 2 * half, E + n_shared, xq.device
     _dev(x_scale, "x_scale", _SCALES, (T, H // 32))
@@ -664,6 +673,7 @@ def layer_few(x, logits, w13, w2, k, method, w13_scale=None, w2_scale=None, n_gr
     _dev(w13, "w13", shape=(G, 2 * I, H // 2 if mx else H))
     _dev(w2, "w2", w13.dtype, (G, H, I // 2 if mx else I))
     if mx:
+        need_mxfp4_types()
         _dev(w13_scale, "w13_scale", _SCALES, (G, 2 * I, H // 32))
         _dev(w2_scale, "w2_scale", _SCALES, (G, H, I // 32))
     elif w13.dtype == torch.float8_e4m3fn:

@@ -35,6 +35,8 @@ class MoELayer:
             raise ValueError("the fused FFN takes a bf16 layer input")
         if mxfp4 and (act_dtype != torch.bfloat16 or fp8_act or fused):
             raise ValueError("4-bit activations take a bf16 layer input, and go with neither fp8_act nor fused")
+        if mxfp4:
+            B.need_mxfp4_types()
         if few and (fp8_act or fused or mxfp4):
             raise ValueError("the layer for few tokens keeps its activations as they are, and is no FFN step")
         if few and T > B.FEW_MAX_T:
