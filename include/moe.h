@@ -600,10 +600,11 @@ moe_status moe_expert_ffn_mxfp4(const uint8_t* xq, const uint8_t* x_scale, int T
  *     ids, scales = moe_route(logits)
  *     y_t = sum_j scales[t,j] W2_e (silu(W1_e x_t) * (W3_e x_t)),  e = ids[t,j]
  *           + the shared experts' rows
- * Each chosen expert's weights are read once.  ids and scales are moe_route's
- * bit for bit.  h is rounded to the activations' type as in moe_expert_ffn; FC2's
- * rows are not rounded but summed in fp32, and y is rounded once, so y is not
- * bit-identical to that of the separate calls.
+ * Each chosen expert's weights are read once for every 16 of its tokens, so those
+ * of an expert with 17 to 32 (a shared one, past 16 tokens) twice.  ids and scales
+ * are moe_route's bit for bit.  h is rounded to the activations' type as in
+ * moe_expert_ffn; FC2's rows are not rounded but summed in fp32, and y is rounded
+ * once, so y is not bit-identical to that of the separate calls.
  *
  *  x         device [T, H] in `act`.
  *  logits, method, k, n_group, topk_group, bias, scaling, flags   as for moe_route.
