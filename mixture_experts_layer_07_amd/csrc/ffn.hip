@@ -146,10 +146,15 @@ __device__ __forceinline__ void store4_bf16(bf16_t* p, const float (&v)[4])
 
 
 // silu(g) with e^-g as one v_exp_f32 of g times a rounded log2(e).  The product's
-// rounding moves silu by at most 0.44 of 2^-24 (g^2 s (1 - s) for s = sigmoid(g)),
-// less than the half-step that a gate of 1 has anyway, and expf costs more
-// where no product runs beside: the epilogue of 256x256 MXFP4 tiles (FC1 of 4096
-// tokens of the Mixtral-shaped layer 610 -> 553 us).
+// rounding (2^-24 of it) and the constant's (0.22 of 2^-24) put e^-g off by 1.22 |g|
+// of 2^-24, and silu by (1 - s) as much, s = sigmoid(g): at most 0.54 of 2^-24
+// absolutely (g^2 s (1 - s) is up to 0.44), but far below zero |g| times a half-step
+// of silu itself, where expf has one or two.  That is less than what the gate's own
+// sum does to e^-g in the same place (K / 64 + 2 half-steps of its terms' sizes, K of
+// 128 and more: 4 |g| at least), and h is rounded to 4 bits next: a code changes only
+// where h is as near to a border as that.  expf costs more where no product runs
+// beside: the epilogue of 256x256 MXFP4 tiles (FC1 of 4096 tokens of the
+// Mixtral-shaped layer 610 -> 553 us).
 __device__ __forceinline__ float silu_exp2(float g)
 {
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.44269504f));
