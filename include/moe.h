@@ -560,7 +560,7 @@ moe_status moe_quantize_mxfp4(const void* x, int dt, int rows, int cols, uint8_t
 /*
  * moe_dequantize_mxfp4 -- the values that codes and scales stand for, in `dt`
  * (MOE_F32 or MOE_BF16): exact, but that a value past the type's range is an
- * infinity (scales above 251 only).  Arguments as for moe_quantize_mxfp4.
+ * infinity (scales above 252 only).  Arguments as for moe_quantize_mxfp4.
  */
 moe_status moe_dequantize_mxfp4(const uint8_t* q, const uint8_t* scale, int rows, int cols, int dt, void* x,
                                 void* stream);
