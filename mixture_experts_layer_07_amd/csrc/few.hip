@@ -20,10 +20,10 @@
 // a piece is multiplied.  A load takes 128 whole bytes of a row in eight lanes: the
 // lane's own row, 64 bytes of 16 rows a load, is what the MFMA takes, but streams
 // 4.5 TB/s where this does 6 to 7, so the lanes of a wave exchange a piece through
-// LDS of their own.  So are the activations: the CU's return path of loads is what
-// bounds the narrow weights (94% busy with MXFP4 when each lane loaded its own
-// fragments of both, 16 loads for 4 KB of weights, where now it is 5 to 8), and
-// where no expert has more than four tokens a piece of theirs is one or two loads.
+// LDS of their own.  So are the activations: loads, not bytes, are what bounds the
+// narrow weights (one token of the DeepSeek-V3-shaped layer in MXFP4: 83 us when each
+// lane loaded its own activations and scales, 16 loads for 4 KB of weights, 56 with 5
+// to 8), and where no expert has more than four tokens a piece of theirs is one or two.
 // The 16 rows of a column tile are the first operand of the MFMA, up to 16 of the
 // expert's tokens the second (rows past the last token repeat it: a column of the
 // result depends on its own token alone).  An expert with 17 to 32 tokens is two chunks,
@@ -333,6 +333,10 @@ __device__ __forceinline__ void run_pipeline(P (&buf)[D], Fetch& fetch, One& one
     }
 }
 
+// h and y in the activations' type.  h is a product's operand next, and rounded here as
+// the experts' FFN in separate calls rounds it: with bf16 the listed layers are 2.3e-3
+// from the exact ones, where y's rounding alone leaves 1.7e-3.  (Two bf16 parts of h would
+// cost FC2 a second product for each fragment and no byte of weights.)
 __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(bf16_t* p, float v) { *p = f32_to_bf16(v); }
 
@@ -423,7 +427,9 @@ __device__ __forceinline__ void fc1_items(const FewArgs& a, const Plan& plan, Su
 }
 
 // MAYBE: an expert may have more than kFew tokens (a call of at most kFew has a
-// kernel of its own, whose smaller stage leaves room for a second workgroup).
+// kernel of its own, whose smaller stage leaves LDS for a second workgroup on the CU;
+// its registers allow one too but with MXFP4 weights in FC1, whose 153 are three waves
+// a SIMD where a workgroup is two: there the CU has one).
 template <class WT, bool MAYBE>
 __global__ __launch_bounds__(kThreads) void few_fc1_kernel(FewArgs a, RouteArgs ra)
 {

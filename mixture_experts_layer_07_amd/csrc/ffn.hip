@@ -483,11 +483,14 @@ __global__ __launch_bounds__(C::NT) void grouped_gemm_kernel(FfnArgs a)
 // for its activations.  FC1's epilogue quantises h per row and 32 channels inside a
 // wave; the staged weight rows are ordered so that a lane holds sixteen neighbouring
 // ones.
-// What bounds the 256x256 tiles is power and LDS: 32x32x64 products of random codes
-// from registers run at 6.2 PFLOP/s on the whole chip, with the six fragments read
-// from LDS that eight of them take here at 5.3, and the K loop's share of FC1 (4096
-// tokens of the Mixtral-shaped layer, 3.4 PFLOP/s in all) comes to 4.7: the rest are
-// tiles' empty rows and the epilogue.
+// What bounds the 256x256 tiles: 32x32x64 products of random codes from registers run at
+// 6.2 PFLOP/s on the whole chip (power), with the six fragments read from LDS that eight of
+// them take here at 5.4.  FC1 of 4096 tokens of the Mixtral-shaped layer reaches 3.25 in all:
+// its large tiles, 526 us of 591, multiply for 40% of their cycles (FC2's 44%; the rows that
+// fill up tiles are 3% of the products).  The rest are the epilogue, the ring's waits, last
+// rounds of the chip that are not full, and the turn to the next tile, where 14 (FC2 20) of
+// the 256 registers are spilt: a reload waits for all of the wave's memory operations, the
+// scale transfers just sent among them.
 template <int BM_, int BN_, int WM_, int WN_, int GM_, int S_, bool W8_ = false, bool A8_ = false, bool A4_ = false>
 struct DmaCfg {
     static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, GM = GM_, S = S_;
@@ -1345,13 +1348,17 @@ moe_status run_classes_a8(const FfnArgs& f, int R, hipStream_t s, int kid)
 // DeepSeek-V3-shaped layer (256 rows a group) 2680 -> 2547 us, 2048 tokens of H 4096,
 // I 2048, E 128 (128 rows) 579 -> 560.  Where they are few, their launch would not fill
 // the chip: 512 tokens of the first layer (16 rows a group) 1069 -> 1146 us, 1024 tokens
-// 1186 -> 1213.
+// 1186 -> 1213.  With even routings of 32 to 96 rows a group no group is past 128, and both
+// rules take the same time within 1% (H 4096, I 2048, E 128 and H 7168, I 2048, E 256); with
+// 128 the first two percent either way, the second 1658 -> 1562 us.
 template <int MODE>
 moe_status run_classes_a4(const FfnArgs& f, int R, hipStream_t s, int kid)
 {
     const long tiles = (long)(R / 256) * (f.N / 256);
     const int big_rows = R / f.G >= 128 && tiles >= 512 ? 129 : kBigRows;
-    const int most = f.T * f.k;  // a class that no group can be of is not launched (2 to 4 us)
+    // A class that no group can be of is not launched: 2 to 3 us of a call, 4 to 6 in a trace.
+    // One that a group could be of and none is costs that (the largest of 512 tokens, each product).
+    const int most = f.T * f.k;
     using Mid = DmaCfg<128, 256, 2, 4, 2, 3, false, false, true>;
     // Where the tiles of all groups are one round of the chip, one launch of them: 333
     // tokens of H 384, I 640, E 12, k 3 44 -> 22 us, 64 of H 2048, I 1408, E 8, k 2 52 -> 29,
