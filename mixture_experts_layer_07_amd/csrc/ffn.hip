@@ -1348,9 +1348,9 @@ moe_status run_classes_a8(const FfnArgs& f, int R, hipStream_t s, int kid)
 // DeepSeek-V3-shaped layer (256 rows a group) 2680 -> 2547 us, 2048 tokens of H 4096,
 // I 2048, E 128 (128 rows) 579 -> 560.  Where they are few, their launch would not fill
 // the chip: 512 tokens of the first layer (16 rows a group) 1069 -> 1146 us, 1024 tokens
-// 1186 -> 1213.  With even routings of 32 to 96 rows a group no group is past 128, and both
-// rules take the same time within 1% (H 4096, I 2048, E 128 and H 7168, I 2048, E 256); with
-// 128 the first two percent either way, the second 1658 -> 1562 us.
+// 1186 -> 1213.  With even routings of 32 to 96 rows a group hardly any is past 128, and
+// 129 and 384 rows as the border take the same time within 2% (H 4096, I 2048, E 128 and
+// H 7168, I 2048, E 256); with 128 rows the first still does, the second 1658 -> 1562 us.
 template <int MODE>
 moe_status run_classes_a4(const FfnArgs& f, int R, hipStream_t s, int kid)
 {
