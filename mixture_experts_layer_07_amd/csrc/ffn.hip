@@ -486,7 +486,7 @@ __global__ __launch_bounds__(C::NT) void grouped_gemm_kernel(FfnArgs a)
 // What bounds the 256x256 tiles: 32x32x64 products of random codes from registers run at
 // 6.2 PFLOP/s on the whole chip (power), with the six fragments read from LDS that eight of
 // them take here at 5.4.  FC1 of 4096 tokens of the Mixtral-shaped layer reaches 3.25 in all:
-// its large tiles, 526 us of 591, multiply for 40% of their cycles (FC2's 44%; the rows that
+// its large tiles, 526 us of 591, multiply for 40% of their cycles (FC2's 45%; the rows that
 // fill up tiles are 3% of the products).  The rest are the epilogue, the ring's waits, last
 // rounds of the chip that are not full, and the turn to the next tile, where 14 (FC2 20) of
 // the 256 registers are spilt: a reload waits for all of the wave's memory operations, the
