@@ -5,11 +5,11 @@
 //   FC2   y[t, n] = sum_j s_tj (h[r_tj] . W2_{e_tj}[n])  (+ shared experts)
 //
 // A few tokens are bound by the weights of the experts that they choose, each read
-// once (twice past 16 tokens of an expert), and by latency.  So the routing of up to eight tokens is done inside FC1, by
-// every workgroup for itself (a wave a token, the tables in LDS), and the weighted sum
-// inside FC2, whose workgroups own output columns and walk through all experts: two
-// launches instead of the five or more of the four-call layer, and no row of FC2 goes
-// through memory.  With more tokens moe_route's kernel goes first, where a wave would
+// once (twice past 16 tokens of an expert), and by latency.  So the routing of up to
+// eight tokens is done inside FC1, by every workgroup for itself (a wave a token, the
+// tables in LDS), and the weighted sum inside FC2, whose workgroups own output columns
+// and walk through all experts: two launches instead of the five or more of the
+// four-call layer, and no row of FC2 goes through memory.  With more tokens moe_route's kernel goes first, where a wave would
 // have had several to route (32 tokens of H 512, I 512, E 256 with groups: 119 us with
 // four a wave, 105 so).  The pairs' rows are numbered as moe_permute numbers them, by
 // expert and token, then those of the shared experts.
